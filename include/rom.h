@@ -459,6 +459,166 @@ int rom_route_dispatch_noalloc(const void* x, int dtype, int64_t T, int Dm, cons
                                int32_t* sorted_slot, int32_t* slot_pos, void* x_sorted,
                                void* stream);
 
+/* ------------------------------------------------------------------------
+ * Around the block: the residual norm in front of it, and its projections on
+ * 8-bit and 4-bit data. The source pages have no counterpart: a Mamba layer
+ * adds the block's output to a residual stream and normalises the sum before
+ * the next block, and low-precision rows and weights are a deployment form of
+ * the same products.
+ *
+ * 8-bit rows ("q8"): e4m3 codes (1 byte each, row-major) with one float32
+ * scale per row; code * scale is the value. The quantisers here write
+ *   a = max(max_c |v_c|, 2^-100),  scale = a / 448,  code = e4m3(v * (448 / a)),
+ * rounded to nearest even; a row of zeros is zeros. A row that holds an
+ * infinity or a NaN gets NaN codes and a NaN scale. Readers take any finite
+ * codes and any scales.
+ * ------------------------------------------------------------------------ */
+
+/*
+ * rom_add_rmsnorm -- residual addition and root-mean-square norm, per row:
+ *   s = x + res (stored in res_out, rounded to its type),
+ *   rstd = 1 / sqrt(sum_c s_c^2 / Dm + eps),   y = s * rstd * w.
+ * The norm is that of s as stored, so that rom_add_rmsnorm_bwd, which reads
+ * the stored s, differentiates the function that ran. Float32 arithmetic (a
+ * row with elements beyond about 1e19 overflows its sum of squares).
+ *
+ *  x        [T][Dm]  dtype
+ *  res      [T][Dm]  res_dtype, or NULL (s = x: the first layer)
+ *  w        [Dm]     float32
+ *  eps               > 0, finite
+ *  res_out  [T][Dm]  out, res_dtype, or NULL; may be the buffer `res`
+ *  y        [T][Dm]  out, dtype, or NULL; may be the buffer `x`
+ *  y8       [T][Dm]  out, e4m3 codes of the (unrounded) y, or NULL
+ *  y_scale  [T]      out, float32, the rows' scales; given exactly when y8 is
+ *  rstd     [T]      out, float32, or NULL (rom_add_rmsnorm_bwd needs it)
+ * res_dtype is ROM_F32, or ROM_BF16 with dtype ROM_BF16. At least one output.
+ * Requires Dm % 8 == 0, Dm <= 16384, T < 2^31 and 16-byte aligned x, res, w,
+ * res_out, y and y8. Buffers overlap only where stated. A row's result does
+ * not depend on the other rows or on T.
+ */
+int rom_add_rmsnorm(const void* x, int dtype, const void* res, int res_dtype, int64_t T, int Dm,
+                    const float* w, float eps, void* res_out, void* y, void* y8, float* y_scale,
+                    float* rstd, void* stream);
+
+/* Bytes of workspace rom_add_rmsnorm_bwd needs for dw (0 for invalid sizes):
+ * at most 512 * Dm * 4. Host function. */
+size_t rom_add_rmsnorm_bwd_workspace_size(int64_t T, int Dm);
+
+/*
+ * rom_add_rmsnorm_bwd -- its gradient. With g = dy * w and s = the forward's
+ * res_out:
+ *   ds = dres_out + rstd * (g - s * rstd^2 * sum_c(g_c s_c) / Dm),
+ *   dw = sum_t dy * s * rstd.
+ * ds is the gradient of x and of res alike.
+ *
+ *  dy       [T][Dm]  dtype: the gradient of y (of the 8-bit rows: that of the
+ *                    values they stand for)
+ *  dres_out [T][Dm]  res_dtype: the gradient of res_out from the layers after
+ *                    this one, or NULL (none)
+ *  res_out  [T][Dm]  res_dtype, and rstd [T]: from the forward
+ *  dx       [T][Dm]  out, ds in dtype, or NULL
+ *  dres     [T][Dm]  out, ds in res_dtype, or NULL; may be the buffer dres_out
+ *  dw       [Dm]     out, float32, or NULL; zeros for T == 0
+ *  ws, ws_bytes      workspace of rom_add_rmsnorm_bwd_workspace_size(T, Dm)
+ *                    bytes, 16-byte aligned (unused without dw)
+ * Sums in float32 in a fixed order (no atomics): the same inputs give the same
+ * bits on the same GPU model. Sizes and alignment as rom_add_rmsnorm.
+ */
+int rom_add_rmsnorm_bwd(const void* dy, int dtype, const void* dres_out, const void* res_out,
+                        int res_dtype, int64_t T, int Dm, const float* w, const float* rstd,
+                        void* dx, void* dres, float* dw, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * rom_quant_rows -- 8-bit rows of a matrix [rows][K] (activations, or expert
+ * weights [E][N][K] as E*N rows: a scale per output feature).
+ *  x      [rows][K]  dtype;  q [rows][K] out, e4m3;  scale [rows] out, float32
+ * Requires K % 8 == 0, K <= 16384, rows < 2^31 and 16-byte aligned x and q.
+ */
+int rom_quant_rows(const void* x, int dtype, int64_t rows, int K, void* q, float* scale,
+                   void* stream);
+
+/*
+ * rom_dispatch_q8 -- rom_dispatch() of 8-bit rows: x8 [T][Dm] e4m3 with x_scale
+ * [T] to x8_sorted [T*k][Dm] and scale_sorted [T*k] in expert order. Other
+ * arguments, checks and outputs as rom_dispatch. Requires Dm % 16 == 0.
+ */
+int rom_dispatch_q8(const void* x8, const float* x_scale, int64_t T, int Dm, int E, int k,
+                    const int32_t* topk_idx, const void* ws, size_t ws_bytes, int32_t* offsets,
+                    int32_t* sorted_slot, int32_t* slot_pos, void* x8_sorted, float* scale_sorted,
+                    void* stream);
+
+/*
+ * rom_expert_proj_q8 -- rom_expert_proj() on 8-bit rows and weights: for the
+ * sorted row p of expert e
+ *   value[p][n] = (sum_c a[p][c] w[e][n][c]) * a_scale[p] * w_scale[e][n],
+ * products of e4m3 codes summed in float32 on the tensor cores, then the
+ * epilogue of `proj` with its outputs in bf16 or float32.
+ *
+ *  proj      as rom_expert_proj; ROM_PROJ_SLOTS without routing arrays is a
+ *            dense projection of the R rows (E == 1)
+ *  a_sorted  [R][K] e4m3;  a_scale [R] float32 (sorted order)
+ *  w0, w1    [E][N][K] e4m3 (w1 for the two Conv+Gate forms);
+ *  w0_scale, w1_scale [E][N] float32
+ *  out       ROM_PROJ_CONV_GATE, k == 1: h_sorted [R][N] bf16; ROM_PROJ_OUT and
+ *            ROM_PROJ_INPROJ, k == 1: [T][N] bf16; otherwise the float32 slot
+ *            rows of rom_expert_proj
+ * Requires K % 16 == 0, N % 128 == 0 and 16-byte aligned a_sorted, w0, w1,
+ * w0_scale, w1_scale and out.
+ */
+int rom_expert_proj_q8(int proj, const void* a_sorted, const float* a_scale, int64_t R, int K,
+                       const void* w0, const float* w0_scale, const void* w1,
+                       const float* w1_scale, int N, int E, int k, const int32_t* offsets,
+                       const int32_t* sorted_slot, const float* topk_w, void* out, void* stream);
+
+/*
+ * 4-bit expert weights ("w4"): w[e][n][c] = (q - 8) * s, q in 0 .. 15, one bf16
+ * scale s for each `group` (32, 64 or 128) consecutive columns of a row. With
+ * Nt = ceil(N / 16) and Kb = ceil(K / 128):
+ *  q  [E][Nt][Kb][1024] bytes: 16 rows x 128 columns per 1 KB tile; row r = 8h + g
+ *     and column c = 32 i + 16 a + 4 t + 2 b + d of the tile (a, b, d in 0 .. 1,
+ *     i, t in 0 .. 3) are bits 4 p .. 4 p + 3, p = 4 d + 2 a + b, of the
+ *     little-endian 32-bit word i of the 16 bytes at h*512 + (4 g + t)*16
+ *  s  [E][Nt][Kb][16][128 / group] bf16
+ * Codes past N and K are 8, their scales 0.
+ */
+
+/* Bytes of q and of s (host functions; 0 for invalid sizes). */
+size_t rom_w4_code_bytes(int E, int N, int K);
+size_t rom_w4_scale_bytes(int E, int N, int K, int group);
+
+/*
+ * rom_quant_expert_weights_w4 -- w [E][N][K] (dtype) to 4 bits: per group
+ * s = bf16(max |w| / 7), q = 8 + round(w / s) clamped to 0 .. 15 (s = 0: q = 8).
+ * A group that holds an infinity or a NaN gets a NaN scale. Requires K % 8 == 0
+ * and 16-byte aligned w, q and s; q and s not overlapping w.
+ */
+int rom_quant_expert_weights_w4(int dtype, const void* w, int E, int N, int K, int group, void* q,
+                                void* s, void* stream);
+
+/*
+ * rom_expert_proj_w4 -- routed projection of T <= 64 tokens on 4-bit weights,
+ * without a dispatch (as rom_expert_proj_dense):
+ *   value[slot] = sum_c x[t][c] w[e][:, c],  slot = t*k + j, e = topk_idx[slot].
+ * Only the experts that some slot selected are read.
+ *
+ *  proj      ROM_PROJ_INPROJ, ROM_PROJ_OUT: value * topk_w[slot], out bf16 [T][N]
+ *            (k == 1) or float32 [T*k][N] in slot order (k > 1);
+ *            ROM_PROJ_SLOTS: float32 slot rows [T*k][N], times topk_w unless NULL;
+ *            ROM_PROJ_CONV_GATE_SLOTS: two matrices, unweighted, float32
+ *            [2][T*k][N] (u from q0, z from q1; topk_w is not read)
+ *  x         [T][K] bf16, token order
+ *  q0, s0, q1, s1  4-bit weights as above (q1, s1 for CONV_GATE_SLOTS, else NULL)
+ *  topk_idx, topk_w [T][k] from rom_route. A slot whose index lies outside
+ *            [0, E) is not written and ROM_ERR_ROUTING is recorded.
+ * Products of codes and activations are exact and summed in float32, a group's
+ * sum is multiplied by its scale in float32, in a fixed order. Any N; requires
+ * K % 8 == 0 and 16-byte aligned x and weights. Launched as a programmatic
+ * dependent of the kernel before it on the stream.
+ */
+int rom_expert_proj_w4(int proj, const void* x, int64_t T, int K, const void* q0, const void* s0,
+                       const void* q1, const void* s1, int N, int E, int k, int group,
+                       const int32_t* topk_idx, const float* topk_w, void* out, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -11,6 +11,8 @@
 // and a per-expert prefix over the 32-slot groups orders the groups. The
 // result needs no atomics on the global order and is deterministic.
 //
+// Rows of 8-bit codes are copied the same way; their scales go with them.
+//
 // Few chunks (small batches, decode): gridDim.y CTAs share a chunk. Each
 // repeats the (cheap) ranking and copies one slice of the row's 16-byte
 // columns; slice 0 writes the index outputs.
@@ -43,7 +45,8 @@ __global__ void __launch_bounds__(kDispatchThreads)
                     const int32_t* __restrict__ topk_idx, const int32_t* __restrict__ chunk_hist,
                     int64_t nchunks, int32_t* __restrict__ offsets,
                     int32_t* __restrict__ sorted_slot, int32_t* __restrict__ slot_pos,
-                    uint4* __restrict__ x_sorted, int* status) {
+                    uint4* __restrict__ x_sorted, const float* __restrict__ x_scale,
+                    float* __restrict__ scale_sorted, int* status) {
   const int slice = blockIdx.y, nslices = gridDim.y;
   __shared__ int s_tot[kMaxExperts];
   __shared__ int s_base[kMaxExperts];
@@ -167,7 +170,10 @@ __global__ void __launch_bounds__(kDispatchThreads)
     for (int e = 0; e < E; ++e) {
       const int p0 = s_off[e] + s_base[e];
       for (int i = warp; i < s_own[e]; i += kDispatchWarps) {
-        if (slice == 0 && lane == 0) sorted_slot[p0 + i] = static_cast<int32_t>(s0);
+        if (slice == 0 && lane == 0) {
+          sorted_slot[p0 + i] = static_cast<int32_t>(s0);
+          if (scale_sorted) scale_sorted[p0 + i] = 0.f;
+        }
         uint4* drow = x_sorted + static_cast<int64_t>(p0 + i) * row_vec16;
         for (int v = v0 + lane; v < v1; v += 32) drow[v] = zero;
       }
@@ -188,6 +194,7 @@ __global__ void __launch_bounds__(kDispatchThreads)
       if (slice == 0) {
         sorted_slot[pos] = static_cast<int32_t>(s0 + ls);
         slot_pos[s0 + ls] = pos;
+        if (scale_sorted) scale_sorted[pos] = x_scale[(s0 + ls) / k];
       }
       s_pos[ls] = pos;
     }
@@ -216,18 +223,15 @@ __global__ void __launch_bounds__(kDispatchThreads)
   }
 }
 
-}  // namespace
-
-cudaError_t launch_dispatch(const void* x, bool bf16, int64_t T, int Dm, int E, int k,
-                            const int32_t* topk_idx, const int32_t* chunk_hist,
-                            int32_t* offsets, int32_t* sorted_slot, int32_t* slot_pos,
-                            void* x_sorted, int* status, cudaStream_t stream) {
+cudaError_t launch_rows(const void* x, int row_bytes, const float* x_scale, int64_t T, int E, int k,
+                        const int32_t* topk_idx, const int32_t* chunk_hist, int32_t* offsets,
+                        int32_t* sorted_slot, int32_t* slot_pos, void* x_sorted,
+                        float* scale_sorted, int* status, cudaStream_t stream) {
   const int64_t nchunks = num_chunks(T);
   if (nchunks == 0) {
     // No tokens: offsets are all zero.
     return cudaMemsetAsync(offsets, 0, sizeof(int32_t) * (E + 1), stream);
   }
-  const int row_bytes = Dm * (bf16 ? 2 : 4);
   // Slices per chunk: enough CTAs to cover the SMs twice, at most 16, and
   // at least 32 vectors (512 bytes) of each row per slice.
   const int64_t want = (2 * static_cast<int64_t>(device_sm_count())) / nchunks;
@@ -254,7 +258,27 @@ cudaError_t launch_dispatch(const void* x, bool bf16, int64_t T, int Dm, int E, 
   cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, dispatch_kernel, static_cast<const uint4*>(x), T,
                             row_bytes / 16, E, k, topk_idx, chunk_hist, nchunks, offsets,
-                            sorted_slot, slot_pos, static_cast<uint4*>(x_sorted), status);
+                            sorted_slot, slot_pos, static_cast<uint4*>(x_sorted), x_scale, scale_sorted,
+                            status);
+}
+
+}  // namespace
+
+cudaError_t launch_dispatch(const void* x, bool bf16, int64_t T, int Dm, int E, int k,
+                            const int32_t* topk_idx, const int32_t* chunk_hist,
+                            int32_t* offsets, int32_t* sorted_slot, int32_t* slot_pos,
+                            void* x_sorted, int* status, cudaStream_t stream) {
+  return launch_rows(x, Dm * (bf16 ? 2 : 4), nullptr, T, E, k, topk_idx, chunk_hist, offsets,
+                     sorted_slot, slot_pos, x_sorted, nullptr, status, stream);
+}
+
+cudaError_t launch_dispatch_q8(const void* x8, const float* x_scale, int64_t T, int Dm, int E,
+                               int k, const int32_t* topk_idx, const int32_t* chunk_hist,
+                               int32_t* offsets, int32_t* sorted_slot, int32_t* slot_pos,
+                               void* x8_sorted, float* scale_sorted, int* status,
+                               cudaStream_t stream) {
+  return launch_rows(x8, Dm, x_scale, T, E, k, topk_idx, chunk_hist, offsets, sorted_slot,
+                     slot_pos, x8_sorted, scale_sorted, status, stream);
 }
 
 }  // namespace rom

@@ -28,6 +28,15 @@
 // Two TMEM accumulators (2 x 256 columns) let the epilogue of one tile run
 // while the MMAs of the next tile proceed. Every wait is bounded.
 // Few routed rows (decode) take a swap-AB kernel instead (below).
+//
+// The same kernels run the products in 8 bits (rom_expert_proj_q8, kQ8): rows
+// and weights in e4m3 with a float32 scale per row and per output feature,
+//   value[p][n] = (sum_c a8[p][c] w8[e][n][c]) * sa[p] * sw[e][n].
+// A 128-byte row of a stage then holds 128 elements of K instead of 64 and one
+// MMA takes 32 of them instead of 16, so tiles, ring, descriptors and barriers
+// are those of bf16 and a stage of the same bytes does twice the work. The
+// scales are constant along K: they multiply the float32 accumulator in the
+// epilogue, before SiLU and before the routing weight.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cudaTypedefs.h>
@@ -42,7 +51,10 @@ namespace rom {
 namespace {
 
 constexpr int BM = 128;
-constexpr int BK = 64;
+constexpr int BKB = 128;  // bytes of K per stage and row: one swizzle row
+constexpr int BK = BKB / 2;
+template <bool kQ8>
+constexpr int kBK = kQ8 ? BKB : BKB / 2;  // elements of K per stage
 constexpr int UMMA_N = 256;
 constexpr uint32_t TMEM_COLS = 2 * UMMA_N;
 constexpr int kThreads = 192;
@@ -67,7 +79,28 @@ struct Params {
   // dense small-batch kernel: weights in the tile-major layout
   // [E][N/128][K/64][128][64] (one 16 KB block per weight tile)
   int w_tiled;
+  // 8-bit products: scales of the sorted rows [R] and of the output features
+  // [E][N] (of W_in and W_g, or of the one matrix)
+  const float* a_scale;
+  const float* w0_scale;
+  const float* w1_scale;
 };
+
+// 8-bit products: acc[j] *= sa * sw[j] for 32 columns, the scales of the
+// columns read as 8 uniform 16-byte loads.
+template <bool kQ8>
+__device__ __forceinline__ void apply_scales(uint32_t (&acc)[32], float sa, const float* sw) {
+  if (kQ8) {
+#pragma unroll
+    for (int v = 0; v < 8; ++v) {
+      const float4 s = __ldg(reinterpret_cast<const float4*>(sw) + v);
+      acc[4 * v + 0] = __float_as_uint(__uint_as_float(acc[4 * v + 0]) * (sa * s.x));
+      acc[4 * v + 1] = __float_as_uint(__uint_as_float(acc[4 * v + 1]) * (sa * s.y));
+      acc[4 * v + 2] = __float_as_uint(__uint_as_float(acc[4 * v + 2]) * (sa * s.z));
+      acc[4 * v + 3] = __float_as_uint(__uint_as_float(acc[4 * v + 3]) * (sa * s.w));
+    }
+  }
+}
 
 // u * SiLU(z) = u * z / (1 + e^-z), with the fast exp and divide intrinsics:
 // their relative error (~1e-6) is far below the bf16 rounding of h (2^-9),
@@ -99,9 +132,13 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
 // float32 outputs (per-slot partials) go row by row through the warp's
 // staging tile `stg` (row-coalesced stores); the bf16 rows, half as wide,
 // are stored directly in 16-byte pieces, which measured faster for them.
-template <int MODE>
+template <int MODE, bool kQ8>
 __device__ __forceinline__ void epilogue_rows(const Params& p, uint32_t t_row, bool valid,
-                                              int64_t prow, int n0, int w, float* stg) {
+                                              int64_t prow, int e, int n0, int w, float* stg) {
+  // this row's scale and the tile's columns' (8-bit products)
+  const float sa = kQ8 && valid ? p.a_scale[prow] : 0.f;
+  const float* sw0 = kQ8 ? p.w0_scale + static_cast<int64_t>(e) * p.N + n0 : nullptr;
+  const float* sw1 = kQ8 && p.w1_scale ? p.w1_scale + static_cast<int64_t>(e) * p.N + n0 : nullptr;
   if (MODE == kEpiGateH) {
     __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out);
 #pragma unroll 1
@@ -110,6 +147,8 @@ __device__ __forceinline__ void epilogue_rows(const Params& p, uint32_t t_row, b
       tmem_ld32(t_row + c * 32, u);
       tmem_ld32(t_row + w + c * 32, z);
       tmem_ld_wait();
+      apply_scales<kQ8>(u, sa, sw0 + c * 32);
+      apply_scales<kQ8>(z, sa, sw1 + c * 32);
       if (valid) {
         uint4* dst = reinterpret_cast<uint4*>(out + prow * p.N + n0 + c * 32);
 #pragma unroll
@@ -136,6 +175,8 @@ __device__ __forceinline__ void epilogue_rows(const Params& p, uint32_t t_row, b
       tmem_ld32(t_row + c * 32, u);
       tmem_ld32(t_row + w + c * 32, z);
       tmem_ld_wait();
+      apply_scales<kQ8>(u, sa, sw0 + c * 32);
+      apply_scales<kQ8>(z, sa, sw1 + c * 32);
       float f[32];
 #pragma unroll
       for (int j = 0; j < 32; ++j) f[j] = __uint_as_float(u[j]);
@@ -154,6 +195,7 @@ __device__ __forceinline__ void epilogue_rows(const Params& p, uint32_t t_row, b
       uint32_t a[32];
       tmem_ld32(t_row + c * 32, a);
       tmem_ld_wait();
+      apply_scales<kQ8>(a, sa, sw0 + c * 32);
       if (MODE == kEpiScaleToken) {
         if (valid) {
           __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out);
@@ -231,7 +273,7 @@ constexpr size_t pair_smem_bytes() {
          (PairGeo<MODE>::kStaged ? 4 * kStageFloats * sizeof(float) : 0) + 1024;
 }
 
-template <int MODE>
+template <int MODE, bool kQ8>
 __global__ void __launch_bounds__(kThreads, 1)
     tc_pair_gemm_kernel(const __grid_constant__ CUtensorMap tmA,
                         const __grid_constant__ CUtensorMap tmB0,
@@ -289,7 +331,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_after();
   const uint32_t tmem_base = ctl.tmem_base;
   const int total = ctl.tile_start[E];
-  const int KB = (p.K + BK - 1) / BK;
+  const int KB = (p.K + kBK<kQ8> - 1) / kBK<kQ8>;
   volatile int* abort_flag = &ctl.abort;
 
   auto coords = [&](int tile, int& e, int& m_blk, int& n_blk) {
@@ -359,8 +401,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           uint8_t* sa = smem + stage * P_STAGE_BYTES;
           const uint32_t fb = full0 + static_cast<uint32_t>(stage * sizeof(uint64_t));
           if (leader) mbar_arrive_expect_tx(&ctl.full[stage], bytes);
-          tma_load_2d_pair(sa, &tmA, fb, kb * BK, row0);
-          tma_load_3d_pair(sa + P_A_BYTES, mb, fb, kb * BK, brow0, e);
+          tma_load_2d_pair(sa, &tmA, fb, kb * kBK<kQ8>, row0);
+          tma_load_3d_pair(sa + P_A_BYTES, mb, fb, kb * kBK<kQ8>, brow0, e);
           issued |= 1u << stage;
           last_par = (last_par & ~(1u << stage)) | (phase << stage);
           if (++stage == P_STAGES) {
@@ -385,8 +427,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp == 1) {
     if (lane == 0 && leader) {
       // ------------------------------------------------ MMA issuer (CTA 0)
-      const uint32_t idesc_whole = idesc_bf16_f32(PM, UMMA_N);
-      const uint32_t idesc_half = idesc_bf16_f32(PM, UMMA_N / 2);
+      const uint32_t idesc_whole = kQ8 ? idesc_e4m3_f32(PM, UMMA_N) : idesc_bf16_f32(PM, UMMA_N);
+      const uint32_t idesc_half =
+          kQ8 ? idesc_e4m3_f32(PM, UMMA_N / 2) : idesc_bf16_f32(PM, UMMA_N / 2);
       int stage = 0;
       uint32_t phase = 0;
       int acc = 0;
@@ -407,9 +450,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint32_t a_addr = smem_u32(smem + stage * P_STAGE_BYTES);
           const uint32_t b_addr = a_addr + P_A_BYTES;
 #pragma unroll
-          for (int kk = 0; kk < BK / 16; ++kk) {
-            mma_bf16_ss_pair(d_tmem, sw128_kmajor_desc(a_addr + kk * 32),
-                             sw128_kmajor_desc(b_addr + kk * 32), idesc, (kb | kk) != 0);
+          for (int kk = 0; kk < BKB / 32; ++kk) {
+            const uint64_t da = sw128_kmajor_desc(a_addr + kk * 32);
+            const uint64_t db = sw128_kmajor_desc(b_addr + kk * 32);
+            if constexpr (kQ8)
+              mma_e4m3_ss_pair(d_tmem, da, db, idesc, (kb | kk) != 0);
+            else
+              mma_bf16_ss_pair(d_tmem, da, db, idesc, (kb | kk) != 0);
           }
           mma_commit_pair_mc(&ctl.empty[stage], 0x3);
           if (++stage == P_STAGES) {
@@ -447,8 +494,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t t_row =
           tmem_base + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(acc * UMMA_N);
       const int w = half < 0 ? kTileN : kTileN / 2;
-      epilogue_rows<MODE>(p, t_row, valid, prow, n_blk * kTileN + (half < 0 ? 0 : half * w), w,
-                          stg);
+      epilogue_rows<MODE, kQ8>(p, t_row, valid, prow, e,
+                               n_blk * kTileN + (half < 0 ? 0 : half * w), w, stg);
       tc_fence_before();
       __syncwarp();
       if (lane == 0) {
@@ -506,7 +553,7 @@ constexpr size_t kSwapSmemBytes = SW_STAGES * SW_STAGE_BYTES + sizeof(SwapCtl) +
 // Output row and router weight of one token of the tile, for the lane that
 // holds it (one token per lane, so the slot and weight loads of a chunk of
 // 32 tokens are issued together rather than one dependent pair per store).
-template <int MODE>
+template <int MODE, bool kQ8>
 __device__ __forceinline__ void swap_token(const Params& p, int64_t prow, bool valid, int& orow,
                                            float& r) {
   orow = 0;
@@ -514,6 +561,7 @@ __device__ __forceinline__ void swap_token(const Params& p, int64_t prow, bool v
   if (valid) {
     const int slot = static_cast<int>(slot_of(p, prow));
     r = p.topk_w ? p.topk_w[slot] : 1.f;  // no routing weights: r = 1
+    if (kQ8) r *= p.a_scale[prow];
     orow = MODE == kEpiScaleToken ? slot / p.k : slot;
   }
 }
@@ -526,7 +574,7 @@ __device__ __forceinline__ void swap_token(const Params& p, int64_t prow, bool v
 // way (each expert's tiles for its single token block), and since nothing
 // before the epilogue depends on the routing, the kernel is launched as a
 // programmatic dependent of the router and only its epilogue waits for it.
-template <int MODE, bool kDense>
+template <int MODE, bool kDense, bool kQ8>
 __global__ void __launch_bounds__(kThreads, 1)
     tc_swap_gemm_kernel(const __grid_constant__ CUtensorMap tmW,
                         const __grid_constant__ CUtensorMap tmX, const Params p) {
@@ -585,7 +633,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_after();
   const uint32_t tmem_base = ctl.tmem_base;
   const int total = ctl.tile_start[E];
-  const int KB = (p.K + BK - 1) / BK;
+  const int KB = (p.K + kBK<kQ8> - 1) / kBK<kQ8>;
   volatile int* abort_flag = &ctl.abort;
   // tile -> (expert, weight-row block, token block); weight-row blocks vary
   // fastest so that CTAs running together share the expert's token rows.
@@ -618,8 +666,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (kDense && p.w_tiled)
             tma_load_5d(sa, &tmW, &ctl.full[stage], 0, 0, kb, w_blk, e);
           else
-            tma_load_3d(sa, &tmW, &ctl.full[stage], kb * BK, n0, e);
-          tma_load_2d(sa + SW_A_BYTES, &tmX, &ctl.full[stage], kb * BK, r0);
+            tma_load_3d(sa, &tmW, &ctl.full[stage], kb * kBK<kQ8>, n0, e);
+          tma_load_2d(sa + SW_A_BYTES, &tmX, &ctl.full[stage], kb * kBK<kQ8>, r0);
           issued |= 1u << stage;
           last_par = (last_par & ~(1u << stage)) | (phase << stage);
           if (++stage == SW_STAGES) {
@@ -634,7 +682,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp == 1) {
     if (lane == 0) {
-      const uint32_t idesc = idesc_bf16_f32(SW_BM, SW_BN);
+      const uint32_t idesc = kQ8 ? idesc_e4m3_f32(SW_BM, SW_BN) : idesc_bf16_f32(SW_BM, SW_BN);
       int stage = 0;
       uint32_t phase = 0;
       int acc = 0;
@@ -653,9 +701,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint32_t a_addr = smem_u32(smem + stage * SW_STAGE_BYTES);
           const uint32_t b_addr = a_addr + SW_A_BYTES;
 #pragma unroll
-          for (int kk = 0; kk < BK / 16; ++kk)
-            mma_bf16_ss(d_tmem, sw128_kmajor_desc(a_addr + kk * 32),
-                        sw128_kmajor_desc(b_addr + kk * 32), idesc, (kb | kk) != 0);
+          for (int kk = 0; kk < BKB / 32; ++kk) {
+            const uint64_t da = sw128_kmajor_desc(a_addr + kk * 32);
+            const uint64_t db = sw128_kmajor_desc(b_addr + kk * 32);
+            if constexpr (kQ8)
+              mma_e4m3_ss(d_tmem, da, db, idesc, (kb | kk) != 0);
+            else
+              mma_bf16_ss(d_tmem, da, db, idesc, (kb | kk) != 0);
+          }
           mma_commit(&ctl.empty[stage]);
           if (++stage == SW_STAGES) {
             stage = 0;
@@ -707,14 +760,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         nv = min(SW_BN, n_e - t_blk * SW_BN);  // valid token columns, >= 1
         // token info first: its loads overlap the wait for the accumulator
         const int64_t prow0 = static_cast<int64_t>(ctl.off[e]) + t_blk * SW_BN;
-        swap_token<MODE>(p, prow0 + lane, lane < nv, orow[0], rw[0]);
-        swap_token<MODE>(p, prow0 + 32 + lane, 32 + lane < nv, orow[1], rw[1]);
+        swap_token<MODE, kQ8>(p, prow0 + lane, lane < nv, orow[0], rw[0]);
+        swap_token<MODE, kQ8>(p, prow0 + 32 + lane, 32 + lane < nv, orow[1], rw[1]);
       }
       if (!mbar_wait(&ctl.tfull[acc], acc_phase, abort_flag, p.status)) break;
       tc_fence_after();
       const uint32_t t_row =
           tmem_base + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(acc * SW_BN);
       const int n = w_blk * SW_BM + q * 32 + lane;  // this thread's output column
+      const float sw = kQ8 ? p.w0_scale[static_cast<int64_t>(e) * p.N + n] : 1.f;
 #pragma unroll
       for (int c = 0; c < SW_BN / 32; ++c) {
         if (32 * c < nv) {  // warp-uniform
@@ -725,7 +779,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int j = 0; j < 32; ++j) {
             if (32 * c + j < nv) {  // warp-uniform
               const int o = __shfl_sync(0xffffffffu, orow[c], j);
-              const float v = __shfl_sync(0xffffffffu, rw[c], j) * __uint_as_float(a[j]);
+              float v = __shfl_sync(0xffffffffu, rw[c], j) * __uint_as_float(a[j]);
+              if (kQ8) v *= sw;
               const bool kept = __shfl_sync(0xffffffffu, keep[c] ? 1 : 0, j) != 0;
               const int64_t i = static_cast<int64_t>(o) * p.N + n;
               if (kept) {
@@ -768,29 +823,33 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
   return fn;
 }
 
-// bf16 tensor map over a row-major [rows][K] matrix (or [E][rows][K] when
-// experts > 0), box of box_rows x 64 elements, 128-byte swizzle.
+// Tensor map over a row-major [rows][K] matrix (or [E][rows][K] when
+// experts > 0) of bf16 or, kQ8, of 8-bit codes: a box of box_rows rows of 128
+// bytes, 128-byte swizzle.
+template <bool kQ8 = false>
 bool make_map(CUtensorMap* m, const void* base, int64_t K, int64_t rows, int experts,
               int box_rows) {
   auto fn = encode_fn();
   if (!fn) return false;
   cuuint64_t dims[3] = {static_cast<cuuint64_t>(K), static_cast<cuuint64_t>(rows),
                         static_cast<cuuint64_t>(experts > 0 ? experts : 1)};
-  cuuint64_t strides[2] = {static_cast<cuuint64_t>(K * 2), static_cast<cuuint64_t>(K * 2 * rows)};
-  cuuint32_t box[3] = {static_cast<cuuint32_t>(BK), static_cast<cuuint32_t>(box_rows), 1};
+  const int64_t es = kQ8 ? 1 : 2;
+  cuuint64_t strides[2] = {static_cast<cuuint64_t>(K * es), static_cast<cuuint64_t>(K * es * rows)};
+  cuuint32_t box[3] = {static_cast<cuuint32_t>(kBK<kQ8>), static_cast<cuuint32_t>(box_rows), 1};
   cuuint32_t estr[3] = {1, 1, 1};
   const cuuint32_t rank = experts > 0 ? 3 : 2;
-  CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, const_cast<void*>(base), dims,
-                  strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+  CUresult r = fn(m, kQ8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank,
+                  const_cast<void*>(base), dims, strides, box, estr,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS;
 }
 
-template <int MODE>
+template <int MODE, bool kQ8>
 cudaError_t launch_pair_mode(const CUtensorMap& a, const CUtensorMap& b0, const CUtensorMap& b1,
                              const CUtensorMap& b0h, const CUtensorMap& b1h, const Params& p,
                              int64_t max_tiles, cudaStream_t stream) {
-  auto kern = tc_pair_gemm_kernel<MODE>;
+  auto kern = tc_pair_gemm_kernel<MODE, kQ8>;
   constexpr size_t kPairSmemBytes = pair_smem_bytes<MODE>();
   cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          static_cast<int>(kPairSmemBytes));
@@ -824,22 +883,25 @@ cudaError_t launch_pair_mode(const CUtensorMap& a, const CUtensorMap& b0, const 
   return cudaLaunchKernelEx(&cfg, kern, a, b0, b1, b0h, b1h, p);
 }
 
-}  // namespace
-
-cudaError_t launch_tc_grouped_gemm(int mode, const void* a_sorted, int64_t R, int K,
-                                   const void* w0, const void* w1, int N, int E, int k,
-                                   const int32_t* offsets, const int32_t* sorted_slot,
-                                   const float* topk_w, void* out, int* status,
-                                   cudaStream_t stream) {
+// The grouped GEMM in bf16, or in 8 bits with the rows' and features' scales.
+template <bool kQ8>
+cudaError_t launch_grouped(int mode, const void* a_sorted, const float* a_scale, int64_t R, int K,
+                           const void* w0, const float* w0_scale, const void* w1,
+                           const float* w1_scale, int N, int E, int k, const int32_t* offsets,
+                           const int32_t* sorted_slot, const float* topk_w, void* out,
+                           int* status, cudaStream_t stream) {
+  constexpr int kAlign = kQ8 ? 16 : 8;  // elements of 16 bytes
   const bool gate = (mode == kEpiGateH || mode == kEpiGateSlots);
   const int tile_n = gate ? 128 : 256;
   // Few tokens (decode): the swap-AB kernel streams every weight tile once.
-  if (!gate && R <= kSwapMaxRows && N % SW_BM == 0 && K % 8 == 0 && E <= kMaxExperts) {
+  if (!gate && R <= kSwapMaxRows && N % SW_BM == 0 && K % kAlign == 0 && E <= kMaxExperts) {
     if (R == 0) return cudaSuccess;
     CUtensorMap tw, tx;
-    if (!make_map(&tw, w0, K, N, E, SW_BM)) return cudaErrorInvalidValue;
-    if (!make_map(&tx, a_sorted, K, R, 0, SW_BN)) return cudaErrorInvalidValue;
+    if (!make_map<kQ8>(&tw, w0, K, N, E, SW_BM)) return cudaErrorInvalidValue;
+    if (!make_map<kQ8>(&tx, a_sorted, K, R, 0, SW_BN)) return cudaErrorInvalidValue;
     Params p{};
+    p.a_scale = a_scale;
+    p.w0_scale = w0_scale;
     p.offsets = offsets;
     p.sorted_slot = sorted_slot;
     p.topk_w = topk_w;
@@ -858,8 +920,8 @@ cudaError_t launch_tc_grouped_gemm(int mode, const void* a_sorted, int64_t R, in
     const int64_t sms = device_sm_count();
     const int64_t per_cta = (tiles_ub + sms - 1) / sms;
     const int grid = static_cast<int>(std::min<int64_t>(sms, (tiles_ub + per_cta - 1) / per_cta));
-    auto kern = (mode == kEpiScaleToken) ? tc_swap_gemm_kernel<kEpiScaleToken, false>
-                                         : tc_swap_gemm_kernel<kEpiScaleSlots, false>;
+    auto kern = (mode == kEpiScaleToken) ? tc_swap_gemm_kernel<kEpiScaleToken, false, kQ8>
+                                         : tc_swap_gemm_kernel<kEpiScaleSlots, false, kQ8>;
     cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                            static_cast<int>(kSwapSmemBytes));
     if (err != cudaSuccess) return err;
@@ -877,18 +939,18 @@ cudaError_t launch_tc_grouped_gemm(int mode, const void* a_sorted, int64_t R, in
     cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, kern, tw, tx, p);
   }
-  if (K % 8 != 0 || N % 128 != 0 || E > kMaxExperts || R >= (int64_t(1) << 31))
+  if (K % kAlign != 0 || N % 128 != 0 || E > kMaxExperts || R >= (int64_t(1) << 31))
     return cudaErrorInvalidValue;
   if (R == 0) return cudaSuccess;
   CUtensorMap ta, tb0, tb1, tb0h, tb1h;
   {
     // B maps: boxes of 128 rows (whole tiles) and 64 rows (half tiles)
-    if (!make_map(&ta, a_sorted, K, R, 0, BM)) return cudaErrorInvalidValue;
-    if (!make_map(&tb0, w0, K, N, E, 128)) return cudaErrorInvalidValue;
-    if (!make_map(&tb0h, w0, K, N, E, 64)) return cudaErrorInvalidValue;
+    if (!make_map<kQ8>(&ta, a_sorted, K, R, 0, BM)) return cudaErrorInvalidValue;
+    if (!make_map<kQ8>(&tb0, w0, K, N, E, 128)) return cudaErrorInvalidValue;
+    if (!make_map<kQ8>(&tb0h, w0, K, N, E, 64)) return cudaErrorInvalidValue;
     if (gate) {
-      if (!make_map(&tb1, w1, K, N, E, 128)) return cudaErrorInvalidValue;
-      if (!make_map(&tb1h, w1, K, N, E, 64)) return cudaErrorInvalidValue;
+      if (!make_map<kQ8>(&tb1, w1, K, N, E, 128)) return cudaErrorInvalidValue;
+      if (!make_map<kQ8>(&tb1h, w1, K, N, E, 64)) return cudaErrorInvalidValue;
     } else {
       tb1 = tb0;
       tb1h = tb0h;
@@ -904,21 +966,45 @@ cudaError_t launch_tc_grouped_gemm(int mode, const void* a_sorted, int64_t R, in
     p.E = E;
     p.k = k;
     p.n_tiles_n = (N + tile_n - 1) / tile_n;
+    p.a_scale = a_scale;
+    p.w0_scale = w0_scale;
+    p.w1_scale = w1_scale;
     p.status = status;
     const int64_t max_tiles = ((R + PM - 1) / PM + E) * static_cast<int64_t>(p.n_tiles_n);
     switch (mode) {
       case kEpiGateH:
-        return launch_pair_mode<kEpiGateH>(ta, tb0, tb1, tb0h, tb1h, p, max_tiles, stream);
+        return launch_pair_mode<kEpiGateH, kQ8>(ta, tb0, tb1, tb0h, tb1h, p, max_tiles, stream);
       case kEpiGateSlots:
-        return launch_pair_mode<kEpiGateSlots>(ta, tb0, tb1, tb0h, tb1h, p, max_tiles, stream);
+        return launch_pair_mode<kEpiGateSlots, kQ8>(ta, tb0, tb1, tb0h, tb1h, p, max_tiles, stream);
       case kEpiScaleToken:
-        return launch_pair_mode<kEpiScaleToken>(ta, tb0, tb1, tb0h, tb1h, p, max_tiles, stream);
+        return launch_pair_mode<kEpiScaleToken, kQ8>(ta, tb0, tb1, tb0h, tb1h, p, max_tiles, stream);
       case kEpiScaleSlots:
-        return launch_pair_mode<kEpiScaleSlots>(ta, tb0, tb1, tb0h, tb1h, p, max_tiles, stream);
+        return launch_pair_mode<kEpiScaleSlots, kQ8>(ta, tb0, tb1, tb0h, tb1h, p, max_tiles, stream);
       default:
         return cudaErrorInvalidValue;
     }
   }
+}
+
+}  // namespace
+
+cudaError_t launch_tc_grouped_gemm(int mode, const void* a_sorted, int64_t R, int K,
+                                   const void* w0, const void* w1, int N, int E, int k,
+                                   const int32_t* offsets, const int32_t* sorted_slot,
+                                   const float* topk_w, void* out, int* status,
+                                   cudaStream_t stream) {
+  return launch_grouped<false>(mode, a_sorted, nullptr, R, K, w0, nullptr, w1, nullptr, N, E, k,
+                               offsets, sorted_slot, topk_w, out, status, stream);
+}
+
+cudaError_t launch_tc_grouped_gemm_q8(int mode, const void* a_sorted, const float* a_scale,
+                                      int64_t R, int K, const void* w0, const float* w0_scale,
+                                      const void* w1, const float* w1_scale, int N, int E, int k,
+                                      const int32_t* offsets, const int32_t* sorted_slot,
+                                      const float* topk_w, void* out, int* status,
+                                      cudaStream_t stream) {
+  return launch_grouped<true>(mode, a_sorted, a_scale, R, K, w0, w0_scale, w1, w1_scale, N, E, k,
+                              offsets, sorted_slot, topk_w, out, status, stream);
 }
 
 cudaError_t launch_tc_dense_small(int mode, const void* x, int64_t T, int K, const void* w, int N,
@@ -964,8 +1050,8 @@ cudaError_t launch_tc_dense_small(int mode, const void* x, int64_t T, int K, con
   const int64_t sms = device_sm_count();
   const int64_t per_cta = (tiles + sms - 1) / sms;
   const int grid = static_cast<int>(std::min<int64_t>(sms, (tiles + per_cta - 1) / per_cta));
-  auto kern = (mode == kEpiScaleToken) ? tc_swap_gemm_kernel<kEpiScaleToken, true>
-                                       : tc_swap_gemm_kernel<kEpiScaleSlots, true>;
+  auto kern = (mode == kEpiScaleToken) ? tc_swap_gemm_kernel<kEpiScaleToken, true, false>
+                                       : tc_swap_gemm_kernel<kEpiScaleSlots, true, false>;
   cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          static_cast<int>(kSwapSmemBytes));
   if (err != cudaSuccess) return err;

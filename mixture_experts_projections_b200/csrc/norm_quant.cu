@@ -1,0 +1,443 @@
+// The norm in front of a block and the 8-bit rows its experts read.
+//
+//   rom_add_rmsnorm       s = x + res (stored in res's type),
+//                         rstd = 1 / sqrt(mean(s^2) + eps), y = s * rstd * w,
+//                         y in x's type and / or as 8-bit rows
+//   rom_add_rmsnorm_bwd   with g = dy * w:
+//                         ds = dres_out + rstd * (g - s * rstd^2 * mean(g * s)),
+//                         dw = sum_t dy * s * rstd
+//   rom_quant_rows        8-bit rows of a matrix
+//
+// 8-bit rows: e4m3 with one float32 scale per row, scale = max(a, 2^-100) / 448
+// with a = max |v| of the row, q = e4m3(v * (448 / max(a, 2^-100))), so that the
+// row's largest value is e4m3's largest (448) and q * scale stands for v. The
+// floor keeps the scale and its reciprocal normal numbers; a row of zeros is
+// zeros. A row that holds an infinity or a NaN has no such scale: its codes and
+// its scale are NaN, so that every product with it is NaN.
+//
+// The norm is that of s as it is stored: the backward has only the stored s,
+// and so differentiates the function that ran. All sums are float32.
+//
+// All three are bound by memory. A row stays in registers between its single
+// read and its writes: one CTA per row, 8 columns (16 bytes of bf16) per
+// thread and step, V steps; short rows take one warp each. The choice goes by
+// the row's length alone, so a row's result does not depend on the batch.
+#include <cuda_bf16.h>
+#include <cuda_fp8.h>
+
+#include <algorithm>
+
+#include "rom_internal.cuh"
+
+namespace rom {
+namespace {
+
+constexpr float kE4m3Max = 448.0f;
+constexpr float kAmaxFloor = 7.888609052210118e-31f;  // 2^-100
+
+__device__ __forceinline__ void load8(const float* p, float (&v)[8]) {
+  const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
+  v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
+  v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+}
+__device__ __forceinline__ void load8(const __nv_bfloat16* p, float (&v)[8]) {
+  const uint4 a = *reinterpret_cast<const uint4*>(p);
+  const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    v[2 * i] = __uint_as_float(w[i] << 16);
+    v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+  }
+}
+__device__ __forceinline__ void store8(float* p, const float (&v)[8]) {
+  reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
+  reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
+}
+__device__ __forceinline__ void store8(__nv_bfloat16* p, const float (&v)[8]) {
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+    w[i] = *reinterpret_cast<const uint32_t*>(&b);
+  }
+  *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+}
+// The value that storing v in T leaves.
+__device__ __forceinline__ float as_stored(float v, const float*) { return v; }
+__device__ __forceinline__ float as_stored(float v, const __nv_bfloat16*) {
+  return __bfloat162float(__float2bfloat16_rn(v));
+}
+
+// A row's threads: one warp (kWarp; blockDim = (32, rows)) or the whole CTA.
+// Sums and maxima over them come back in every thread; the order of the
+// additions is fixed. `red` holds one value per warp and is written once per
+// kernel (or between barriers of the caller).
+template <bool kWarp>
+__device__ __forceinline__ float row_sum(float v, float* red) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  if (kWarp) return v;
+  const int warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
+  if ((threadIdx.x & 31) == 0) red[warp] = v;
+  __syncthreads();
+  float s = 0.f;
+  for (int i = 0; i < nw; ++i) s += red[i];
+  return s;
+}
+template <bool kWarp>
+__device__ __forceinline__ uint32_t row_max(uint32_t v, uint32_t* red) {
+  v = __reduce_max_sync(0xffffffffu, v);
+  if (kWarp) return v;
+  const int warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
+  if ((threadIdx.x & 31) == 0) red[warp] = v;
+  __syncthreads();
+  uint32_t s = 0;
+  for (int i = 0; i < nw; ++i) s = max(s, red[i]);
+  return s;
+}
+
+// Bits of |v|: they order as the values do, and a NaN above all of them.
+__device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7fffffffu; }
+
+// The row's scale and the factor of its codes from the bits of max |v|.
+__device__ __forceinline__ void row_scale(uint32_t amax_bits, float& scale, float& inv) {
+  if (amax_bits >= 0x7f800000u) {
+    scale = inv = __uint_as_float(0x7fffffffu);
+  } else {
+    const float a = fmaxf(__uint_as_float(amax_bits), kAmaxFloor);
+    scale = __fdiv_rn(a, kE4m3Max);
+    inv = __fdiv_rn(kE4m3Max, a);
+  }
+}
+
+// 8 codes. |v * inv| is at most 448 (1 + 2^-22), which rounds to 448.
+__device__ __forceinline__ void store_codes(uint8_t* p, const float (&v)[8], float inv) {
+  uint32_t w[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(v[4 * i] * inv, v[4 * i + 1] * inv),
+                                                 __NV_SATFINITE, __NV_E4M3);
+    const uint32_t hi = __nv_cvt_float2_to_fp8x2(
+        make_float2(v[4 * i + 2] * inv, v[4 * i + 3] * inv), __NV_SATFINITE, __NV_E4M3);
+    w[i] = lo | (hi << 16);
+  }
+  *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
+}
+
+template <typename XT, typename RT, int V, bool kWarp>
+__global__ void __launch_bounds__(512)
+    add_rmsnorm_kernel(const XT* x, const RT* res, int64_t T, int D,
+                                   const float* __restrict__ w, float eps, RT* res_out, XT* y,
+                                   uint8_t* __restrict__ y8, float* __restrict__ y_scale,
+                                   float* __restrict__ rstd_out) {
+  __shared__ float red[32];
+  __shared__ uint32_t redm[32];
+  const int64_t row =
+      kWarp ? blockIdx.x * static_cast<int64_t>(blockDim.y) + threadIdx.y : blockIdx.x;
+  if (kWarp && row >= T) return;
+  const int step = kWarp ? 32 : blockDim.x;
+  const int64_t base = row * D;
+  float s[V][8];
+  float sum = 0.f;
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    const int c = (threadIdx.x + i * step) * 8;
+    if (c < D) {
+      load8(x + base + c, s[i]);
+      if (res) {
+        float r[8];
+        load8(res + base + c, r);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) s[i][j] += r[j];
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        s[i][j] = as_stored(s[i][j], res_out);
+        sum = fmaf(s[i][j], s[i][j], sum);
+      }
+    }
+  }
+  sum = row_sum<kWarp>(sum, red);
+  const float rstd = rsqrtf(sum / static_cast<float>(D) + eps);
+  if (threadIdx.x == 0 && rstd_out) rstd_out[row] = rstd;
+  uint32_t amax = 0;
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    const int c = (threadIdx.x + i * step) * 8;
+    if (c < D) {
+      if (res_out) store8(res_out + base + c, s[i]);
+      float wv[8];
+      load8(w + c, wv);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        s[i][j] = s[i][j] * rstd * wv[j];
+        amax = max(amax, abs_bits(s[i][j]));
+      }
+      if (y) store8(y + base + c, s[i]);
+    }
+  }
+  if (y8) {
+    amax = row_max<kWarp>(amax, redm);
+    float scale, inv;
+    row_scale(amax, scale, inv);
+    if (threadIdx.x == 0) y_scale[row] = scale;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int c = (threadIdx.x + i * step) * 8;
+      if (c < D) store_codes(y8 + base + c, s[i], inv);
+    }
+  }
+}
+
+template <typename XT, int V, bool kWarp>
+__global__ void __launch_bounds__(512)
+    quant_rows_kernel(const XT* __restrict__ x, int64_t rows, int D,
+                                  uint8_t* __restrict__ q, float* __restrict__ scale_out) {
+  __shared__ uint32_t redm[32];
+  const int64_t row =
+      kWarp ? blockIdx.x * static_cast<int64_t>(blockDim.y) + threadIdx.y : blockIdx.x;
+  if (kWarp && row >= rows) return;
+  const int step = kWarp ? 32 : blockDim.x;
+  const int64_t base = row * D;
+  float s[V][8];
+  uint32_t amax = 0;
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    const int c = (threadIdx.x + i * step) * 8;
+    if (c < D) {
+      load8(x + base + c, s[i]);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) amax = max(amax, abs_bits(s[i][j]));
+    }
+  }
+  amax = row_max<kWarp>(amax, redm);
+  float scale, inv;
+  row_scale(amax, scale, inv);
+  if (threadIdx.x == 0) scale_out[row] = scale;
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    const int c = (threadIdx.x + i * step) * 8;
+    if (c < D) store_codes(q + base + c, s[i], inv);
+  }
+}
+
+// CTA b takes rows b, b + gridDim.x, ...; a thread's columns stay its own, so
+// that it adds up their dw over its CTA's rows in registers. The CTA's sums go
+// to row b of the workspace, and dw_reduce_kernel adds them in row order: no
+// atomics, the same result every time.
+template <typename XT, typename RT, int V>
+__global__ void __launch_bounds__(512)
+    add_rmsnorm_bwd_kernel(const XT* __restrict__ dy, const RT* dres_out,
+                                       const RT* __restrict__ s, int64_t T, int D,
+                                       const float* __restrict__ w,
+                                       const float* __restrict__ rstd, XT* __restrict__ dx,
+                                       RT* dres, float* __restrict__ dw_part) {
+  __shared__ float red[2][32];
+  float dw[V][8];
+#pragma unroll
+  for (int i = 0; i < V; ++i)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) dw[i][j] = 0.f;
+  const float inv_d = 1.f / static_cast<float>(D);
+  int buf = 0;
+  for (int64_t row = blockIdx.x; row < T; row += gridDim.x, buf ^= 1) {
+    const int64_t base = row * D;
+    const float r = rstd[row];
+    float g[V][8], sv[V][8];
+    float dot = 0.f;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int c = (threadIdx.x + i * blockDim.x) * 8;
+      if (c < D) {
+        float wv[8];
+        load8(dy + base + c, g[i]);
+        load8(s + base + c, sv[i]);
+        load8(w + c, wv);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          dw[i][j] = fmaf(g[i][j], sv[i][j] * r, dw[i][j]);
+          g[i][j] *= wv[j];
+          dot = fmaf(g[i][j], sv[i][j], dot);
+        }
+      }
+    }
+    // two buffers: a warp may still read this row's sums when another one
+    // writes the next row's, never two rows on
+    dot = row_sum<false>(dot, red[buf]);
+    const float k = r * r * (dot * inv_d);
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int c = (threadIdx.x + i * blockDim.x) * 8;
+      if (c < D) {
+        float d[8];
+        if (dres_out) {
+          load8(dres_out + base + c, d);
+        } else {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) d[j] = 0.f;
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) d[j] = fmaf(r, fmaf(-sv[i][j], k, g[i][j]), d[j]);
+        if (dx) store8(dx + base + c, d);
+        if (dres) store8(dres + base + c, d);
+      }
+    }
+  }
+  if (dw_part) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int c = (threadIdx.x + i * blockDim.x) * 8;
+      if (c < D) store8(dw_part + static_cast<int64_t>(blockIdx.x) * D + c, dw[i]);
+    }
+  }
+}
+
+// dw[c] = sum over the P rows of part, 32 columns per CTA: 8 warps take every
+// eighth row each, and their sums are added in warp order.
+__global__ void __launch_bounds__(256)
+    dw_reduce_kernel(const float* __restrict__ part, int P, int D, float* __restrict__ dw) {
+  __shared__ float sum[8][32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int c = blockIdx.x * 32 + lane;
+  float v = 0.f;
+  if (c < D)
+    for (int p = warp; p < P; p += 8) v += part[static_cast<int64_t>(p) * D + c];
+  sum[warp][lane] = v;
+  __syncthreads();
+  if (warp == 0 && c < D) {
+    float t = sum[0][lane];
+    for (int i = 1; i < 8; ++i) t += sum[i][lane];
+    dw[c] = t;
+  }
+}
+
+// Steps per thread (V) and the launch of one row's threads for D columns:
+// rows of up to 512 columns take a warp, up to 4096 columns one step of a CTA
+// with a thread for each 8 columns, longer ones more steps.
+struct RowShape {
+  int V;
+  bool warp;
+  dim3 block;
+};
+RowShape row_shape(int D) {
+  const int nvec = D / 8;
+  if (nvec <= 64) return {nvec <= 32 ? 1 : 2, true, dim3(32, 8, 1)};
+  int V = 1;
+  while (nvec > V * 512 && V < 4) V *= 2;
+  const int threads = ((nvec + V - 1) / V + 31) / 32 * 32;
+  return {V, false, dim3(static_cast<unsigned>(threads), 1, 1)};
+}
+
+template <typename XT, typename RT>
+cudaError_t add_rmsnorm(const void* x, const void* res, int64_t T, int D, const float* w,
+                        float eps, void* res_out, void* y, void* y8, float* y_scale, float* rstd,
+                        cudaStream_t stream) {
+  const RowShape sh = row_shape(D);
+  const unsigned grid = static_cast<unsigned>(sh.warp ? (T + 7) / 8 : T);
+  auto go = [&](auto kern) {
+    kern<<<grid, sh.block, 0, stream>>>(
+        static_cast<const XT*>(x), static_cast<const RT*>(res), T, D, w, eps,
+        static_cast<RT*>(res_out), static_cast<XT*>(y), static_cast<uint8_t*>(y8), y_scale, rstd);
+    return cudaGetLastError();
+  };
+  if (sh.warp)
+    return sh.V == 1 ? go(add_rmsnorm_kernel<XT, RT, 1, true>)
+                     : go(add_rmsnorm_kernel<XT, RT, 2, true>);
+  switch (sh.V) {
+    case 1:
+      return go(add_rmsnorm_kernel<XT, RT, 1, false>);
+    case 2:
+      return go(add_rmsnorm_kernel<XT, RT, 2, false>);
+    default:
+      return go(add_rmsnorm_kernel<XT, RT, 4, false>);
+  }
+}
+
+template <typename XT>
+cudaError_t quant_rows(const void* x, int64_t rows, int D, void* q, float* scale,
+                       cudaStream_t stream) {
+  const RowShape sh = row_shape(D);
+  const unsigned grid = static_cast<unsigned>(sh.warp ? (rows + 7) / 8 : rows);
+  auto go = [&](auto kern) {
+    kern<<<grid, sh.block, 0, stream>>>(static_cast<const XT*>(x), rows, D,
+                                        static_cast<uint8_t*>(q), scale);
+    return cudaGetLastError();
+  };
+  if (sh.warp)
+    return sh.V == 1 ? go(quant_rows_kernel<XT, 1, true>) : go(quant_rows_kernel<XT, 2, true>);
+  switch (sh.V) {
+    case 1:
+      return go(quant_rows_kernel<XT, 1, false>);
+    case 2:
+      return go(quant_rows_kernel<XT, 2, false>);
+    default:
+      return go(quant_rows_kernel<XT, 4, false>);
+  }
+}
+
+template <typename XT, typename RT>
+cudaError_t add_rmsnorm_bwd(const void* dy, const void* dres_out, const void* s, int64_t T, int D,
+                            const float* w, const float* rstd, void* dx, void* dres, float* dw,
+                            float* ws, cudaStream_t stream) {
+  const int nvec = D / 8;
+  int V = 1;
+  while (nvec > V * 512 && V < 4) V *= 2;
+  const int threads = ((nvec + V - 1) / V + 31) / 32 * 32;
+  const int64_t grid = std::min<int64_t>({T, kNormBwdMaxParts,
+                                          static_cast<int64_t>(device_sm_count()) *
+                                              std::max(1, 1024 / threads)});
+  auto go = [&](auto kern) {
+    kern<<<static_cast<unsigned>(grid), threads, 0, stream>>>(
+        static_cast<const XT*>(dy), static_cast<const RT*>(dres_out), static_cast<const RT*>(s), T,
+        D, w, rstd, static_cast<XT*>(dx), static_cast<RT*>(dres), dw ? ws : nullptr);
+    return cudaGetLastError();
+  };
+  cudaError_t err;
+  switch (V) {
+    case 1:
+      err = go(add_rmsnorm_bwd_kernel<XT, RT, 1>);
+      break;
+    case 2:
+      err = go(add_rmsnorm_bwd_kernel<XT, RT, 2>);
+      break;
+    default:
+      err = go(add_rmsnorm_bwd_kernel<XT, RT, 4>);
+  }
+  if (err != cudaSuccess || !dw) return err;
+  dw_reduce_kernel<<<static_cast<unsigned>((D + 31) / 32), 256, 0, stream>>>(
+      ws, static_cast<int>(grid), D, dw);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_add_rmsnorm(const void* x, bool x_bf16, const void* res, bool res_bf16,
+                               int64_t T, int D, const float* w, float eps, void* res_out, void* y,
+                               void* y8, float* y_scale, float* rstd, cudaStream_t stream) {
+  if (x_bf16)
+    return res_bf16 ? add_rmsnorm<__nv_bfloat16, __nv_bfloat16>(x, res, T, D, w, eps, res_out, y,
+                                                                y8, y_scale, rstd, stream)
+                    : add_rmsnorm<__nv_bfloat16, float>(x, res, T, D, w, eps, res_out, y, y8,
+                                                        y_scale, rstd, stream);
+  return add_rmsnorm<float, float>(x, res, T, D, w, eps, res_out, y, y8, y_scale, rstd, stream);
+}
+
+cudaError_t launch_add_rmsnorm_bwd(const void* dy, bool x_bf16, const void* dres_out,
+                                   const void* s, bool res_bf16, int64_t T, int D, const float* w,
+                                   const float* rstd, void* dx, void* dres, float* dw, float* ws,
+                                   cudaStream_t stream) {
+  if (x_bf16)
+    return res_bf16 ? add_rmsnorm_bwd<__nv_bfloat16, __nv_bfloat16>(dy, dres_out, s, T, D, w, rstd,
+                                                                    dx, dres, dw, ws, stream)
+                    : add_rmsnorm_bwd<__nv_bfloat16, float>(dy, dres_out, s, T, D, w, rstd, dx,
+                                                            dres, dw, ws, stream);
+  return add_rmsnorm_bwd<float, float>(dy, dres_out, s, T, D, w, rstd, dx, dres, dw, ws, stream);
+}
+
+cudaError_t launch_quant_rows(const void* x, bool x_bf16, int64_t rows, int D, void* q,
+                              float* scale, cudaStream_t stream) {
+  return x_bf16 ? quant_rows<__nv_bfloat16>(x, rows, D, q, scale, stream)
+                : quant_rows<float>(x, rows, D, q, scale, stream);
+}
+
+}  // namespace rom

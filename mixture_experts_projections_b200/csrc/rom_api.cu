@@ -26,6 +26,17 @@ int current_device() {
   return d;
 }
 
+// A buffer's bytes; a null one overlaps nothing.
+struct Span {
+  const void* p;
+  size_t bytes;
+};
+bool overlap(const Span& a, const Span& b) {
+  if (!a.p || !b.p || a.bytes == 0 || b.bytes == 0) return false;
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
+  return x < y + b.bytes && y < x + a.bytes;
+}
+
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 int to_status(cudaError_t e) {
@@ -77,6 +88,8 @@ int device_sm_count() {
 }  // namespace rom
 
 using rom::aligned16;
+using rom::overlap;
+using rom::Span;
 
 extern "C" {
 
@@ -386,6 +399,210 @@ int rom_debug_wait_timeout(uint64_t limit_ns, void* stream) {
   if (!st) return ROM_ERR_CUDA;
   rom::debug_wait_kernel<<<1, 32, 0, static_cast<cudaStream_t>(stream)>>>(limit_ns, st);
   return rom::to_status(cudaGetLastError());
+}
+
+int rom_add_rmsnorm(const void* x, int dtype, const void* res, int res_dtype, int64_t T, int Dm,
+                    const float* w, float eps, void* res_out, void* y, void* y8, float* y_scale,
+                    float* rstd, void* stream) {
+  if ((dtype != ROM_F32 && dtype != ROM_BF16) || (res_dtype != ROM_F32 && res_dtype != ROM_BF16))
+    return ROM_ERR_INVALID_ARG;
+  if (T < 0 || Dm <= 0 || !(eps > 0.f) || eps > 3.4e38f) return ROM_ERR_INVALID_ARG;
+  if (!y8 != !y_scale) return ROM_ERR_INVALID_ARG;
+  if (dtype == ROM_F32 && res_dtype != ROM_F32) return ROM_ERR_UNSUPPORTED;
+  if (Dm % 8 != 0 || Dm > rom::kNormMaxCols || T >= (int64_t(1) << 31)) return ROM_ERR_UNSUPPORTED;
+  if (T == 0) return ROM_OK;
+  if (!x || !w || (!res_out && !y && !y8 && !rstd)) return ROM_ERR_INVALID_ARG;
+  if (!aligned16(x) || !aligned16(res) || !aligned16(w) || !aligned16(res_out) || !aligned16(y) ||
+      !aligned16(y8))
+    return ROM_ERR_UNSUPPORTED;
+  // outputs overlap nothing, but for res_out on res and y on x as a whole
+  const size_t n = static_cast<size_t>(T) * Dm;
+  const size_t xb = n * (dtype == ROM_BF16 ? 2 : 4), rb = n * (res_dtype == ROM_BF16 ? 2 : 4);
+  const Span in[] = {{x, xb}, {res, rb}, {w, sizeof(float) * Dm}};
+  const Span out[] = {{res_out, rb}, {y, xb}, {y8, n}, {y_scale, sizeof(float) * T},
+                      {rstd, sizeof(float) * T}};
+  for (int i = 0; i < 5; ++i) {
+    for (int j = 0; j < 3; ++j) {
+      const bool same = (i == 0 && j == 1 && res_out == res) || (i == 1 && j == 0 && y == x);
+      if (!same && overlap(out[i], in[j])) return ROM_ERR_INVALID_ARG;
+    }
+    for (int j = 0; j < i; ++j)
+      if (overlap(out[i], out[j])) return ROM_ERR_INVALID_ARG;
+  }
+  return rom::to_status(rom::launch_add_rmsnorm(x, dtype == ROM_BF16, res, res_dtype == ROM_BF16,
+                                                T, Dm, w, eps, res_out, y, y8, y_scale, rstd,
+                                                static_cast<cudaStream_t>(stream)));
+}
+
+size_t rom_add_rmsnorm_bwd_workspace_size(int64_t T, int Dm) {
+  if (T <= 0 || Dm <= 0) return 0;
+  const int64_t parts = T < rom::kNormBwdMaxParts ? T : rom::kNormBwdMaxParts;
+  return static_cast<size_t>(parts) * static_cast<size_t>(Dm) * sizeof(float);
+}
+
+int rom_add_rmsnorm_bwd(const void* dy, int dtype, const void* dres_out, const void* res_out,
+                        int res_dtype, int64_t T, int Dm, const float* w, const float* rstd,
+                        void* dx, void* dres, float* dw, void* ws, size_t ws_bytes, void* stream) {
+  if ((dtype != ROM_F32 && dtype != ROM_BF16) || (res_dtype != ROM_F32 && res_dtype != ROM_BF16))
+    return ROM_ERR_INVALID_ARG;
+  if (T < 0 || Dm <= 0) return ROM_ERR_INVALID_ARG;
+  if (dtype == ROM_F32 && res_dtype != ROM_F32) return ROM_ERR_UNSUPPORTED;
+  if (Dm % 8 != 0 || Dm > rom::kNormMaxCols || T >= (int64_t(1) << 31)) return ROM_ERR_UNSUPPORTED;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (T == 0) {
+    if (dw && cudaMemsetAsync(dw, 0, sizeof(float) * Dm, s) != cudaSuccess) return ROM_ERR_CUDA;
+    return ROM_OK;
+  }
+  if (!dy || !res_out || !w || !rstd || (!dx && !dres && !dw)) return ROM_ERR_INVALID_ARG;
+  if (!aligned16(dy) || !aligned16(dres_out) || !aligned16(res_out) || !aligned16(w) ||
+      !aligned16(dx) || !aligned16(dres) || !aligned16(ws))
+    return ROM_ERR_UNSUPPORTED;
+  const size_t need = rom_add_rmsnorm_bwd_workspace_size(T, Dm);
+  if (dw && (!ws || ws_bytes < need)) return ROM_ERR_WORKSPACE;
+  const size_t n = static_cast<size_t>(T) * Dm;
+  const size_t xb = n * (dtype == ROM_BF16 ? 2 : 4), rb = n * (res_dtype == ROM_BF16 ? 2 : 4);
+  const Span in[] = {{dy, xb}, {dres_out, rb}, {res_out, rb}, {w, sizeof(float) * Dm},
+                     {rstd, sizeof(float) * T}};
+  const Span out[] = {{dx, xb}, {dres, rb}, {dw, sizeof(float) * Dm}, {dw ? ws : nullptr, need}};
+  for (int i = 0; i < 4; ++i) {
+    for (int j = 0; j < 5; ++j) {
+      const bool same = i == 1 && j == 1 && dres == dres_out;
+      if (!same && overlap(out[i], in[j])) return ROM_ERR_INVALID_ARG;
+    }
+    for (int j = 0; j < i; ++j)
+      if (overlap(out[i], out[j])) return ROM_ERR_INVALID_ARG;
+  }
+  return rom::to_status(rom::launch_add_rmsnorm_bwd(dy, dtype == ROM_BF16, dres_out, res_out,
+                                                    res_dtype == ROM_BF16, T, Dm, w, rstd, dx,
+                                                    dres, dw, static_cast<float*>(ws), s));
+}
+
+int rom_quant_rows(const void* x, int dtype, int64_t rows, int K, void* q, float* scale,
+                   void* stream) {
+  if (dtype != ROM_F32 && dtype != ROM_BF16) return ROM_ERR_INVALID_ARG;
+  if (rows < 0 || K <= 0) return ROM_ERR_INVALID_ARG;
+  if (K % 8 != 0 || K > rom::kNormMaxCols || rows >= (int64_t(1) << 31)) return ROM_ERR_UNSUPPORTED;
+  if (rows == 0) return ROM_OK;
+  if (!x || !q || !scale) return ROM_ERR_INVALID_ARG;
+  if (!aligned16(x) || !aligned16(q)) return ROM_ERR_UNSUPPORTED;
+  const size_t n = static_cast<size_t>(rows) * K;
+  const Span xs = {x, n * (dtype == ROM_BF16 ? 2 : 4)}, qs = {q, n},
+             ss = {scale, sizeof(float) * rows};
+  if (overlap(xs, qs) || overlap(xs, ss) || overlap(qs, ss)) return ROM_ERR_INVALID_ARG;
+  return rom::to_status(rom::launch_quant_rows(x, dtype == ROM_BF16, rows, K, q, scale,
+                                               static_cast<cudaStream_t>(stream)));
+}
+
+int rom_dispatch_q8(const void* x8, const float* x_scale, int64_t T, int Dm, int E, int k,
+                    const int32_t* topk_idx, const void* ws, size_t ws_bytes, int32_t* offsets,
+                    int32_t* sorted_slot, int32_t* slot_pos, void* x8_sorted, float* scale_sorted,
+                    void* stream) {
+  if (T < 0 || Dm <= 0 || E < 1 || E > rom::kMaxExperts || k < 1 || k > E || k > rom::kMaxTopK)
+    return ROM_ERR_INVALID_ARG;
+  if (T * k >= (int64_t(1) << 31) || Dm % 16 != 0) return ROM_ERR_UNSUPPORTED;
+  if (!offsets) return ROM_ERR_INVALID_ARG;
+  if (T > 0) {
+    if (!x8 || !x_scale || !topk_idx || !sorted_slot || !slot_pos || !x8_sorted || !scale_sorted)
+      return ROM_ERR_INVALID_ARG;
+    if (!aligned16(x8) || !aligned16(x8_sorted)) return ROM_ERR_UNSUPPORTED;
+    if (!ws || ws_bytes < rom_workspace_size(T, E)) return ROM_ERR_WORKSPACE;
+  }
+  int* st = rom::status_ptr();
+  if (!st) return ROM_ERR_CUDA;
+  return rom::to_status(rom::launch_dispatch_q8(x8, x_scale, T, Dm, E, k, topk_idx,
+                                                static_cast<const int32_t*>(ws), offsets,
+                                                sorted_slot, slot_pos, x8_sorted, scale_sorted, st,
+                                                static_cast<cudaStream_t>(stream)));
+}
+
+int rom_expert_proj_q8(int proj, const void* a_sorted, const float* a_scale, int64_t R, int K,
+                       const void* w0, const float* w0_scale, const void* w1,
+                       const float* w1_scale, int N, int E, int k, const int32_t* offsets,
+                       const int32_t* sorted_slot, const float* topk_w, void* out, void* stream) {
+  if (proj != ROM_PROJ_CONV_GATE && proj != ROM_PROJ_OUT && proj != ROM_PROJ_INPROJ &&
+      proj != ROM_PROJ_SLOTS && proj != ROM_PROJ_CONV_GATE_SLOTS)
+    return ROM_ERR_INVALID_ARG;
+  if (R < 0 || K <= 0 || N <= 0 || E < 1 || E > rom::kMaxExperts || k < 1 || k > E ||
+      k > rom::kMaxTopK || R % k != 0)
+    return ROM_ERR_INVALID_ARG;
+  if (R >= (int64_t(1) << 31) || K % 16 != 0 || N % 128 != 0) return ROM_ERR_UNSUPPORTED;
+  if (R == 0) return ROM_OK;
+  const bool gate = proj == ROM_PROJ_CONV_GATE || proj == ROM_PROJ_CONV_GATE_SLOTS;
+  const bool gate_slots = proj == ROM_PROJ_CONV_GATE_SLOTS || (gate && k > 1);
+  const bool slots = proj == ROM_PROJ_SLOTS;
+  const bool dense = slots && !offsets && !sorted_slot;  // no routing arrays, one matrix
+  if (dense && E != 1) return ROM_ERR_INVALID_ARG;
+  if ((!offsets && !dense) || !w0 || !w0_scale || (gate && (!w1 || !w1_scale)))
+    return ROM_ERR_INVALID_ARG;
+  if (!gate && !dense && (!sorted_slot || (!slots && !topk_w))) return ROM_ERR_INVALID_ARG;
+  if (gate_slots && !sorted_slot) return ROM_ERR_INVALID_ARG;
+  if (!a_sorted || !a_scale || !out) return ROM_ERR_INVALID_ARG;
+  if (!aligned16(a_sorted) || !aligned16(w0) || !aligned16(w0_scale) || !aligned16(out) ||
+      (gate && (!aligned16(w1) || !aligned16(w1_scale))))
+    return ROM_ERR_UNSUPPORTED;
+  const int mode = gate    ? (gate_slots ? rom::kEpiGateSlots : rom::kEpiGateH)
+                   : slots ? rom::kEpiScaleSlots
+                           : (k == 1 ? rom::kEpiScaleToken : rom::kEpiScaleSlots);
+  int* st = rom::status_ptr();
+  if (!st) return ROM_ERR_CUDA;
+  return rom::to_status(rom::launch_tc_grouped_gemm_q8(
+      mode, a_sorted, a_scale, R, K, w0, w0_scale, gate ? w1 : nullptr, gate ? w1_scale : nullptr,
+      N, E, k, offsets, sorted_slot, topk_w, out, st, static_cast<cudaStream_t>(stream)));
+}
+
+size_t rom_w4_code_bytes(int E, int N, int K) {
+  if (E < 1 || N <= 0 || K <= 0) return 0;
+  return static_cast<size_t>(E) * ((static_cast<size_t>(N) + 15) / 16) *
+         ((static_cast<size_t>(K) + 127) / 128) * 1024;
+}
+
+size_t rom_w4_scale_bytes(int E, int N, int K, int group) {
+  if (group != 32 && group != 64 && group != 128) return 0;
+  return rom_w4_code_bytes(E, N, K) / 1024 * 16 * (128 / group) * 2;
+}
+
+int rom_quant_expert_weights_w4(int dtype, const void* w, int E, int N, int K, int group, void* q,
+                                void* s, void* stream) {
+  if (dtype != ROM_F32 && dtype != ROM_BF16) return ROM_ERR_INVALID_ARG;
+  if (E < 1 || N <= 0 || K <= 0 || (group != 32 && group != 64 && group != 128))
+    return ROM_ERR_INVALID_ARG;
+  const size_t qb = rom_w4_code_bytes(E, N, K), sb = rom_w4_scale_bytes(E, N, K, group);
+  // one warp per 1 KB tile, eight to a block
+  if (K % 8 != 0 || qb / 1024 >= (size_t(1) << 33) || N > (1 << 30) || K > (1 << 30))
+    return ROM_ERR_UNSUPPORTED;
+  if (!w || !q || !s) return ROM_ERR_INVALID_ARG;
+  if (!aligned16(w) || !aligned16(q) || !aligned16(s)) return ROM_ERR_UNSUPPORTED;
+  const Span wv = {w, static_cast<size_t>(E) * N * K * (dtype == ROM_BF16 ? 2 : 4)}, qv = {q, qb},
+             sv = {s, sb};
+  if (overlap(wv, qv) || overlap(wv, sv) || overlap(qv, sv)) return ROM_ERR_INVALID_ARG;
+  return rom::to_status(rom::launch_quant_w4(w, dtype == ROM_BF16, E, N, K, group, q, s,
+                                             static_cast<cudaStream_t>(stream)));
+}
+
+int rom_expert_proj_w4(int proj, const void* x, int64_t T, int K, const void* q0, const void* s0,
+                       const void* q1, const void* s1, int N, int E, int k, int group,
+                       const int32_t* topk_idx, const float* topk_w, void* out, void* stream) {
+  const bool gate = proj == ROM_PROJ_CONV_GATE_SLOTS;
+  const bool slots = proj == ROM_PROJ_SLOTS;
+  if (!gate && !slots && proj != ROM_PROJ_OUT && proj != ROM_PROJ_INPROJ)
+    return ROM_ERR_INVALID_ARG;
+  if (T < 0 || K <= 0 || N <= 0 || E < 1 || E > rom::kMaxExperts || k < 1 || k > E ||
+      k > rom::kMaxTopK || (group != 32 && group != 64 && group != 128))
+    return ROM_ERR_INVALID_ARG;
+  if (gate != (q1 != nullptr) || gate != (s1 != nullptr)) return ROM_ERR_INVALID_ARG;
+  if (T > 64 || K % 8 != 0 || N > (1 << 30) || K > (1 << 30)) return ROM_ERR_UNSUPPORTED;
+  if (T == 0) return ROM_OK;
+  if (!x || !q0 || !s0 || !topk_idx || !out || (!gate && !slots && !topk_w))
+    return ROM_ERR_INVALID_ARG;
+  if (!aligned16(x) || !aligned16(q0) || !aligned16(s0) || !aligned16(q1) || !aligned16(s1))
+    return ROM_ERR_UNSUPPORTED;
+  const bool to_token = !gate && !slots && k == 1;
+  if ((reinterpret_cast<uintptr_t>(out) & (to_token ? 1u : 3u)) != 0) return ROM_ERR_UNSUPPORTED;
+  int* st = rom::status_ptr();
+  if (!st) return ROM_ERR_CUDA;
+  return rom::to_status(rom::launch_w4_proj(x, static_cast<int>(T), K, q0, s0, q1, s1, N, E, k,
+                                            group, topk_idx, gate ? nullptr : topk_w, out,
+                                            to_token, st, static_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

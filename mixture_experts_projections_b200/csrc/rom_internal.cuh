@@ -64,6 +64,12 @@ cudaError_t launch_dispatch(const void* x, bool bf16, int64_t T, int Dm, int E, 
                             const int32_t* topk_idx, const int32_t* chunk_hist,
                             int32_t* offsets, int32_t* sorted_slot, int32_t* slot_pos,
                             void* x_sorted, int* status, cudaStream_t stream);
+// The same for rows of 8-bit codes (Dm bytes) with a scale each.
+cudaError_t launch_dispatch_q8(const void* x8, const float* x_scale, int64_t T, int Dm, int E,
+                               int k, const int32_t* topk_idx, const int32_t* chunk_hist,
+                               int32_t* offsets, int32_t* sorted_slot, int32_t* slot_pos,
+                               void* x8_sorted, float* scale_sorted, int* status,
+                               cudaStream_t stream);
 
 // Epilogue variants of the grouped GEMMs.
 enum EpiMode : int {
@@ -80,6 +86,15 @@ cudaError_t launch_tc_grouped_gemm(int mode, const void* a_sorted, int64_t R, in
                                    const int32_t* offsets, const int32_t* sorted_slot,
                                    const float* topk_w, void* out, int* status,
                                    cudaStream_t stream);
+
+// The same on e4m3 rows and weights with float32 scales per sorted row and per
+// output feature.
+cudaError_t launch_tc_grouped_gemm_q8(int mode, const void* a_sorted, const float* a_scale,
+                                      int64_t R, int K, const void* w0, const float* w0_scale,
+                                      const void* w1, const float* w1_scale, int N, int E, int k,
+                                      const int32_t* offsets, const int32_t* sorted_slot,
+                                      const float* topk_w, void* out, int* status,
+                                      cudaStream_t stream);
 
 // Small-batch (T <= 64) routed projection without a dispatch: x in token
 // order, the router's topk_idx / topk_w read only by the epilogue.
@@ -98,6 +113,27 @@ cudaError_t launch_simt_grouped_gemm(int mode, const float* a_sorted, int64_t R,
 
 cudaError_t launch_combine(int mode, bool bf16, const float* in, int64_t T, int k, int N,
                            const int32_t* slot_pos, void* out, cudaStream_t stream);
+
+// ---- norm and 8-bit rows (norm_quant.cu)
+constexpr int kNormMaxCols = 16384;           // columns of a row
+constexpr int64_t kNormBwdMaxParts = 512;     // workspace rows of the norm's dw
+cudaError_t launch_add_rmsnorm(const void* x, bool x_bf16, const void* res, bool res_bf16,
+                               int64_t T, int D, const float* w, float eps, void* res_out, void* y,
+                               void* y8, float* y_scale, float* rstd, cudaStream_t stream);
+cudaError_t launch_add_rmsnorm_bwd(const void* dy, bool x_bf16, const void* dres_out,
+                                   const void* s, bool res_bf16, int64_t T, int D, const float* w,
+                                   const float* rstd, void* dx, void* dres, float* dw, float* ws,
+                                   cudaStream_t stream);
+cudaError_t launch_quant_rows(const void* x, bool x_bf16, int64_t rows, int D, void* q,
+                              float* scale, cudaStream_t stream);
+
+// ---- 4-bit weights (w4_proj.cu); q1/s1: a second matrix (Conv+Gate), else null
+cudaError_t launch_w4_proj(const void* x, int T, int K, const void* q0, const void* s0,
+                           const void* q1, const void* s1, int N, int E, int k, int group,
+                           const int32_t* topk_idx, const float* topk_w, void* out, bool to_token,
+                           int* status, cudaStream_t stream);
+cudaError_t launch_quant_w4(const void* w, bool bf16, int E, int N, int K, int group, void* q,
+                            void* s, cudaStream_t stream);
 
 cudaError_t launch_debug_wait(uint64_t limit_ns, int* status, cudaStream_t stream);
 

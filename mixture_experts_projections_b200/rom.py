@@ -58,6 +58,19 @@ SIGNATURES = {
                                  _I, _I, _P, _P, _P, _P, ctypes.c_size_t, _P]),
     "rom_ssm_core": (_I, [_P, _L, _I, _I, _P, _P, _I, _P, _I, _I, _I, _P, _P, _P, _P, _P, _P,
                           ctypes.c_size_t, _P]),
+    "rom_add_rmsnorm": (_I, [_P, _I, _P, _I, _L, _I, _P, ctypes.c_float, _P, _P, _P, _P, _P, _P]),
+    "rom_add_rmsnorm_bwd_workspace_size": (ctypes.c_size_t, [_L, _I]),
+    "rom_add_rmsnorm_bwd": (_I, [_P, _I, _P, _P, _I, _L, _I, _P, _P, _P, _P, _P, _P,
+                                 ctypes.c_size_t, _P]),
+    "rom_quant_rows": (_I, [_P, _I, _L, _I, _P, _P, _P]),
+    "rom_dispatch_q8": (_I, [_P, _P, _L, _I, _I, _I, _P, _P, ctypes.c_size_t, _P, _P, _P, _P, _P,
+                             _P]),
+    "rom_expert_proj_q8": (_I, [_I, _P, _P, _L, _I, _P, _P, _P, _P, _I, _I, _I, _P, _P, _P, _P,
+                                _P]),
+    "rom_w4_code_bytes": (ctypes.c_size_t, [_I, _I, _I]),
+    "rom_w4_scale_bytes": (ctypes.c_size_t, [_I, _I, _I, _I]),
+    "rom_quant_expert_weights_w4": (_I, [_I, _P, _I, _I, _I, _I, _P, _P, _P]),
+    "rom_expert_proj_w4": (_I, [_I, _P, _L, _I, _P, _P, _P, _P, _I, _I, _I, _I, _P, _P, _P, _P]),
 }
 
 _lib = None
@@ -203,6 +216,200 @@ def rom_route_dispatch_noalloc(x, w_r, bias, k, renorm, topk_idx, topk_w, counts
         _ptr(x), _dtype_code(x), T, Dm, _ptr(w_r), _ptr(bias), E, k, int(renorm),
         _ptr(topk_idx), _ptr(topk_w), _ptr(counts), _ptr(offsets), _ptr(sorted_slot),
         _ptr(slot_pos), _ptr(x_sorted), _stream(stream)), "rom_route_dispatch_noalloc")
+
+
+# ------------------------------------------------------------------ norm, 8-bit and 4-bit data
+#
+# These entry points check every tensor (type, shape, contiguity, one device)
+# before the library is called, run on the tensors' device whichever device is
+# current, and take the current stream of that device unless given one.
+
+
+def _t(t, name, dtype, *shape):
+    """Refuses a tensor of another type, shape or layout, or on the CPU;
+    returns its address."""
+    if t.dtype is not dtype or t.shape != shape:
+        raise RomError(f"{name} must be {dtype} {list(shape)}, got {t.dtype} {list(t.shape)}")
+    if not t.is_cuda or not t.is_contiguous():
+        raise RomError(f"{name} must be a contiguous CUDA tensor")
+    return t.data_ptr()
+
+
+def _call(fn, stream, tensors, *args):
+    """Calls a library function with the stream as its last argument, on the
+    device of ``tensors`` (which must all be the same)."""
+    index = None
+    for t in tensors:
+        if t is not None:
+            i = t.get_device()
+            if index is None:
+                index = i
+            elif i != index:
+                raise RomError(f"{fn}: tensors on different devices (cuda:{index}, cuda:{i})")
+    if stream is None:
+        stream = torch.cuda.current_stream(index)
+    elif stream.device.index != index:
+        raise RomError(f"{fn}: the stream is not one of cuda:{index}")
+    lib = _lib or load_library()
+    if torch.cuda.current_device() == index:
+        code = getattr(lib, fn)(*args, stream.cuda_stream)
+    else:
+        with torch.cuda.device(index):
+            code = getattr(lib, fn)(*args, stream.cuda_stream)
+    if code != ROM_OK:
+        _check(code, fn)
+
+
+_BF16, _F32, _I32, _E4M3 = torch.bfloat16, torch.float32, torch.int32, torch.float8_e4m3fn
+
+
+def rom_add_rmsnorm(x, residual, weight, eps, res_out, y, y8=None, y_scale=None, rstd=None,
+                    stream=None):
+    """s = x + residual (to ``res_out``, may be ``residual``), y = s * rstd *
+    weight with rstd = 1 / sqrt(mean s^2 + eps), per row of [T, Dm]. Any of the
+    outputs may be None; ``y8`` (e4m3) and ``y_scale`` come together. The
+    residual stream's type is that of ``residual`` or ``res_out``."""
+    T, D = x.shape
+    rt = residual.dtype if residual is not None else (res_out.dtype if res_out is not None else _F32)
+    code = _dtype_code(x)
+    _call("rom_add_rmsnorm", stream, (x, residual, weight, res_out, y, y8, y_scale, rstd),
+          _t(x, "x", x.dtype, T, D), code,
+          None if residual is None else _t(residual, "residual", rt, T, D),
+          ROM_BF16 if rt is _BF16 else ROM_F32 if rt is _F32 else -1, T, D,
+          _t(weight, "weight", _F32, D), eps,
+          None if res_out is None else _t(res_out, "res_out", rt, T, D),
+          None if y is None else _t(y, "y", x.dtype, T, D),
+          None if y8 is None else _t(y8, "y8", _E4M3, T, D),
+          None if y_scale is None else _t(y_scale, "y_scale", _F32, T),
+          None if rstd is None else _t(rstd, "rstd", _F32, T))
+
+
+def rom_add_rmsnorm_bwd_workspace_size(T: int, D: int) -> int:
+    return int(load_library().rom_add_rmsnorm_bwd_workspace_size(T, D))
+
+
+def rom_add_rmsnorm_bwd(dy, dres_out, res_out, weight, rstd, dx, dres, dw, ws, stream=None):
+    """Gradient of rom_add_rmsnorm: dx (type of dy) and dres (type of res_out,
+    may be ``dres_out``) are the same values, dw float32 [Dm]; each may be
+    None, and so may ``dres_out``. ``ws``: at least
+    rom_add_rmsnorm_bwd_workspace_size(T, Dm) bytes, for dw."""
+    T, D = dy.shape
+    rt = res_out.dtype
+    code = _dtype_code(dy)
+    if ws is not None and not (ws.is_cuda and ws.is_contiguous()):
+        raise RomError("ws must be a contiguous CUDA tensor")
+    _call("rom_add_rmsnorm_bwd", stream, (dy, dres_out, res_out, weight, rstd, dx, dres, dw, ws),
+          _t(dy, "dy", dy.dtype, T, D), code,
+          None if dres_out is None else _t(dres_out, "dres_out", rt, T, D),
+          _t(res_out, "res_out", rt, T, D),
+          ROM_BF16 if rt is _BF16 else ROM_F32 if rt is _F32 else -1, T, D,
+          _t(weight, "weight", _F32, D), _t(rstd, "rstd", _F32, T),
+          None if dx is None else _t(dx, "dx", dy.dtype, T, D),
+          None if dres is None else _t(dres, "dres", rt, T, D),
+          None if dw is None else _t(dw, "dw", _F32, D),
+          None if ws is None else ws.data_ptr(),
+          0 if ws is None else ws.numel() * ws.element_size())
+
+
+def rom_quant_rows(x, q, scale, stream=None):
+    """The rows of x [rows, K] as e4m3 codes ``q`` and a float32 scale each."""
+    rows, K = x.shape
+    code = _dtype_code(x)
+    _call("rom_quant_rows", stream, (x, q, scale), _t(x, "x", x.dtype, rows, K), code, rows, K,
+          _t(q, "q", _E4M3, rows, K), _t(scale, "scale", _F32, rows))
+
+
+def rom_dispatch_q8(x8, x_scale, E, k, topk_idx, ws, offsets, sorted_slot, slot_pos, x8_sorted,
+                    scale_sorted, stream=None):
+    T, D = x8.shape
+    R = T * k
+    n = max(R, 1)
+    if ws is not None and not (ws.is_cuda and ws.is_contiguous()):
+        raise RomError("ws must be a contiguous CUDA tensor")
+    _call("rom_dispatch_q8", stream,
+          (x8, x_scale, topk_idx, ws, offsets, sorted_slot, slot_pos, x8_sorted, scale_sorted),
+          _t(x8, "x8", _E4M3, T, D), _t(x_scale, "x_scale", _F32, T), T, D, E, k,
+          _t(topk_idx, "topk_idx", _I32, T, k), None if ws is None else ws.data_ptr(),
+          0 if ws is None else ws.numel() * ws.element_size(), _t(offsets, "offsets", _I32, E + 1),
+          _t(sorted_slot, "sorted_slot", _I32, n), _t(slot_pos, "slot_pos", _I32, n),
+          _t(x8_sorted, "x8_sorted", _E4M3, n, D), _t(scale_sorted, "scale_sorted", _F32, n))
+
+
+def rom_expert_proj_q8(proj, a_sorted, a_scale, w0, w0_scale, w1, w1_scale, k, offsets,
+                       sorted_slot, topk_w, out, stream=None):
+    """rom_expert_proj on e4m3 rows [R, K] and weights [E, N, K] with float32
+    scales [R] and [E, N]. ``out`` as there, in bf16 or (slot rows) float32."""
+    R, K = a_sorted.shape
+    E, N, _ = w0.shape
+    gate = proj == ROM_PROJ_CONV_GATE or proj == ROM_PROJ_CONV_GATE_SLOTS
+    if gate and (w1 is None or w1_scale is None):
+        raise RomError("the Conv+Gate projections need w1 and w1_scale")
+    if k < 1 or R % k:
+        raise RomError(f"{R} rows are no multiple of k = {k}")
+    if k == 1 and (proj == ROM_PROJ_OUT or proj == ROM_PROJ_INPROJ or proj == ROM_PROJ_CONV_GATE):
+        po = _t(out, "out", _BF16, R, N)
+    else:
+        shape = (2, R, N) if gate else (R, N)
+        po = _t(out, "out", _F32, *shape)
+    dense = offsets is None
+    if sorted_slot is not None and sorted_slot.shape[0] < R:
+        raise RomError(f"sorted_slot must hold {R} slots")
+    if topk_w is not None and topk_w.numel() != R:
+        raise RomError(f"topk_w must hold {R} weights")
+    _call("rom_expert_proj_q8", stream,
+          (a_sorted, a_scale, w0, w0_scale, w1, w1_scale, offsets, sorted_slot, topk_w, out),
+          proj, _t(a_sorted, "a_sorted", _E4M3, R, K), _t(a_scale, "a_scale", _F32, R), R, K,
+          _t(w0, "w0", _E4M3, E, N, K), _t(w0_scale, "w0_scale", _F32, E, N),
+          _t(w1, "w1", _E4M3, E, N, K) if gate else None,
+          _t(w1_scale, "w1_scale", _F32, E, N) if gate else None, N, E, k,
+          None if dense else _t(offsets, "offsets", _I32, E + 1),
+          None if sorted_slot is None else _t(sorted_slot, "sorted_slot", _I32,
+                                              sorted_slot.shape[0]),
+          None if topk_w is None else _t(topk_w, "topk_w", _F32, *topk_w.shape), po)
+
+
+def rom_quant_expert_weights_w4(w, group, q, s, stream=None):
+    """w [E, N, K] (bf16 or float32) to 4-bit codes ``q`` uint8 [E, Nt, Kb, 2, 8,
+    4, 16] and bf16 scales ``s`` [E, Nt, Kb, 16, 128 / group] (Nt = ceil(N / 16),
+    Kb = ceil(K / 128); the layout is in include/rom.h)."""
+    E, N, K = w.shape
+    if group not in (32, 64, 128):
+        raise RomError(f"group must be 32, 64 or 128, got {group}")
+    nt, kb = -(-N // 16), -(-K // 128)
+    code = _dtype_code(w)
+    _call("rom_quant_expert_weights_w4", stream, (w, q, s), code, _t(w, "w", w.dtype, E, N, K), E,
+          N, K, group, _t(q, "q", torch.uint8, E, nt, kb, 2, 8, 4, 16),
+          _t(s, "s", _BF16, E, nt, kb, 16, 128 // group))
+
+
+def rom_expert_proj_w4(proj, x, q0, s0, q1, s1, N, k, topk_idx, topk_w, out, stream=None):
+    """Routed projection of T <= 64 tokens x [T, K] (bf16) on 4-bit weights, in
+    token order without a dispatch. ROM_PROJ_OUT and ROM_PROJ_INPROJ: weighted,
+    out bf16 [T, N] (k == 1) or float32 [T*k, N]; ROM_PROJ_SLOTS: float32
+    [T*k, N]; ROM_PROJ_CONV_GATE_SLOTS (with q1, s1): float32 [2, T*k, N]."""
+    T, K = x.shape
+    E, nt, kb = q0.shape[:3]
+    if nt != -(-N // 16) or kb != -(-K // 128):
+        raise RomError(f"q0 {list(q0.shape)} does not hold {N} x {K} weights")
+    groups = s0.shape[-1]
+    if groups not in (1, 2, 4):
+        raise RomError("s0 must hold 1, 2 or 4 scales per row and tile")
+    gate = proj == ROM_PROJ_CONV_GATE_SLOTS
+    if gate != (q1 is not None) or gate != (s1 is not None):
+        raise RomError("q1 and s1 go with ROM_PROJ_CONV_GATE_SLOTS, and only with it")
+    if gate:
+        po = _t(out, "out", _F32, 2, T * k, N)
+    elif k == 1 and proj != ROM_PROJ_SLOTS:
+        po = _t(out, "out", _BF16, T, N)
+    else:
+        po = _t(out, "out", _F32, T * k, N)
+    qs, ss = (E, nt, kb, 2, 8, 4, 16), (E, nt, kb, 16, groups)
+    _call("rom_expert_proj_w4", stream, (x, q0, s0, q1, s1, topk_idx, topk_w, out), proj,
+          _t(x, "x", _BF16, T, K), T, K, _t(q0, "q0", torch.uint8, *qs), _t(s0, "s0", _BF16, *ss),
+          _t(q1, "q1", torch.uint8, *qs) if gate else None,
+          _t(s1, "s1", _BF16, *ss) if gate else None, N, E, k, 128 // groups,
+          _t(topk_idx, "topk_idx", _I32, T, k),
+          None if topk_w is None else _t(topk_w, "topk_w", _F32, T, k), po)
 
 
 # ------------------------------------------------------------------ block helpers
@@ -397,7 +604,7 @@ def block_forward(x, w_r, bias, w_conv, w_gate, w_out, k, renorm=False, bufs=Non
 
 
 def inproj_forward(x, w_r, w, k=1, renorm=False, bias=None, bufs=None, out=None, slots=None,
-                   stream=None, dense_small=True, w_tiled=None):
+                   stream=None, dense_small=True, w_tiled=None, w_q4=None):
     """Swimba routed in-projection: s_t = sum_j r_{t,j} x_t W_{S_j} (W as [E, N, Dm]).
 
     A bf16 batch of at most DENSE_SMALL_MAX_TOKENS tokens (a decode step)
@@ -405,10 +612,14 @@ def inproj_forward(x, w_r, w, k=1, renorm=False, bias=None, bufs=None, out=None,
     ``dense_small`` is False; the router then forms neither the per-expert
     counts nor the per-chunk histograms (``bufs.counts`` is left as it was),
     which only a dispatch needs. ``w_tiled`` (pack_expert_weights(w)), when
-    given, is what that path reads instead of ``w``."""
+    given, is what that path reads instead of ``w``. ``w_q4`` (W4Weights):
+    the projection runs on the 4-bit weights instead, 64 tokens at a time for
+    any T, and ``w`` may be None."""
     T, Dm = x.shape
-    E, N, _ = w.shape
     R = T * k
+    if w_q4 is not None:
+        return _inproj_forward_w4(x, w_r, w_q4, k, renorm, bias, bufs, out, slots, stream)
+    E, N, _ = w.shape
     if out is None:
         out = torch.empty((T, N), dtype=x.dtype, device=x.device)
     if dense_small and x.dtype == torch.bfloat16 and 0 < T <= DENSE_SMALL_MAX_TOKENS:
@@ -438,6 +649,321 @@ def inproj_forward(x, w_r, w, k=1, renorm=False, bias=None, bufs=None, out=None,
                         rb.sorted_slot, rb.topk_w, slots, stream)
         rom_combine(ROM_COMBINE_SUM, _dtype_code(x), slots, T, k, N, None, out, stream)
     return out, rb
+
+
+def _inproj_forward_w4(x, w_r, w, k, renorm, bias, bufs, out, slots, stream):
+    T, Dm = x.shape
+    _t(x, "x", _BF16, T, w.K)
+    _t(w_r, "w_r", _F32, Dm, w.E)
+    with _scope(x, stream):
+        if bufs is None:
+            bufs = RoutingBuffers(T, Dm, w.E, k, x.dtype, x.device)
+        if out is None:
+            out = torch.empty((T, w.N), dtype=x.dtype, device=x.device)
+        if k > 1 and slots is None:
+            slots = torch.empty((T * k, w.N), dtype=torch.float32, device=x.device)
+        rom_route(x, w_r, bias, k, renorm, bufs.topk_idx, bufs.topk_w, None, None, stream)
+        _w4_tokens(ROM_PROJ_INPROJ, x, w, None, k, bufs.topk_idx, bufs.topk_w,
+                   out if k == 1 else slots, stream)
+        if k > 1:
+            rom_combine(ROM_COMBINE_SUM, _dtype_code(x), slots, T, k, w.N, None, out, stream)
+    return out, bufs
+
+
+# ------------------------------------------------------------------ norm, 8-bit and 4-bit blocks
+
+
+def _scope(t, stream):
+    """Runs the library on the device of ``t`` and on ``stream`` (None: that
+    device's current one). Buffers that the functions below make belong to that
+    stream, so that their memory is never still in use on another one."""
+    return torch.cuda.device(t.device) if stream is None else torch.cuda.stream(stream)
+
+
+def quant_rows(x, stream=None):
+    """(codes e4m3 [rows, K], scales float32 [rows]) of x [rows, K]: 8-bit rows
+    with code * scale standing for the value."""
+    with _scope(x, stream):
+        q = torch.empty(x.shape, dtype=torch.float8_e4m3fn, device=x.device)
+        scale = torch.empty(x.shape[:1], dtype=torch.float32, device=x.device)
+        rom_quant_rows(x, q, scale, stream)
+    return q, scale
+
+
+class Q8Weights:
+    """Expert weights [E, N, K] in 8 bits: ``q`` e4m3 and ``scale`` float32
+    [E, N], one per output feature."""
+
+    def __init__(self, q, scale):
+        self.q, self.scale = q, scale
+        self.E, self.N, self.K = q.shape
+
+    @classmethod
+    def quantize(cls, w, stream=None):
+        """From weights [E, N, K] in bf16 or float32 (the library layout)."""
+        E, N, K = w.shape
+        q, scale = quant_rows(w.view(E * N, K), stream)
+        return cls(q.view(E, N, K), scale.view(E, N))
+
+
+class W4Weights:
+    """Expert weights [E, N, K] in 4 bits with a bf16 scale per ``group``
+    columns, in the tiled storage of include/rom.h (``q`` and ``s``)."""
+
+    def __init__(self, q, s, N, K):
+        self.q, self.s, self.N, self.K = q, s, N, K
+        self.E = q.shape[0]
+        self.group = 128 // s.shape[-1]
+
+    @classmethod
+    def quantize(cls, w, group=128, stream=None):
+        """From weights [E, N, K] in bf16 or float32 (the library layout)."""
+        E, N, K = w.shape
+        if group not in (32, 64, 128):
+            raise RomError(f"group must be 32, 64 or 128, got {group}")
+        nt, kb = -(-N // 16), -(-K // 128)
+        with _scope(w, stream):
+            q = torch.empty((E, nt, kb, 2, 8, 4, 16), dtype=torch.uint8, device=w.device)
+            s = torch.empty((E, nt, kb, 16, 128 // group), dtype=torch.bfloat16, device=w.device)
+            rom_quant_expert_weights_w4(w, group, q, s, stream)
+        return cls(q, s, N, K)
+
+
+# Tokens of one rom_expert_proj_w4 call.
+W4_MAX_TOKENS = 64
+
+
+def _w4_tokens(proj, x, w0, w1, k, topk_idx, topk_w, out, stream):
+    """rom_expert_proj_w4 for any number of tokens, 64 at a time. ``out`` holds
+    the rows of all tokens (or slots); two matrices write out[0] and out[1]."""
+    T = x.shape[0]
+    for a in range(0, T, W4_MAX_TOKENS):
+        b = min(T, a + W4_MAX_TOKENS)
+        idx, r = topk_idx[a:b], topk_w[a:b]
+        if proj == ROM_PROJ_CONV_GATE_SLOTS and T > W4_MAX_TOKENS:
+            # u and z of a part of the tokens are not contiguous together
+            for w, o in ((w0, out[0]), (w1, out[1])):
+                rom_expert_proj_w4(ROM_PROJ_SLOTS, x[a:b], w.q, w.s, None, None, w.N, k, idx, None,
+                                   o[a * k:b * k], stream)
+        elif proj == ROM_PROJ_CONV_GATE_SLOTS:
+            rom_expert_proj_w4(proj, x, w0.q, w0.s, w1.q, w1.s, w0.N, k, idx, None, out, stream)
+        else:
+            rows = out[a * k:b * k]
+            rom_expert_proj_w4(proj, x[a:b], w0.q, w0.s, None, None, w0.N, k, idx, r, rows, stream)
+
+
+class NormBuffers:
+    """Outputs of the residual norm: ``residual`` (the new residual stream),
+    ``y`` (the block's input), ``rstd``, and with ``q8`` the 8-bit rows ``y8``
+    and their scales ``y_scale``."""
+
+    def __init__(self, T, D, dtype, residual_dtype, device, q8=False):
+        self.residual = torch.empty((T, D), dtype=residual_dtype, device=device)
+        self.y = torch.empty((T, D), dtype=dtype, device=device)
+        self.rstd = torch.empty((T,), dtype=torch.float32, device=device)
+        self.y8 = torch.empty((T, D), dtype=torch.float8_e4m3fn, device=device) if q8 else None
+        self.y_scale = torch.empty((T,), dtype=torch.float32, device=device) if q8 else None
+
+
+def add_rmsnorm(x, residual, weight, eps=1e-5, q8=False, residual_dtype=torch.float32, bufs=None,
+                stream=None):
+    """Residual addition and norm in front of a block (rom_add_rmsnorm). ``x``
+    [T, Dm] is the block output before it (or the embeddings, with ``residual``
+    None: the residual stream then starts in ``residual_dtype``). Returns
+    NormBuffers."""
+    T, D = x.shape
+    if bufs is None:
+        rt = residual_dtype if residual is None else residual.dtype
+        with _scope(x, stream):
+            bufs = NormBuffers(T, D, x.dtype, rt, x.device, q8)
+    rom_add_rmsnorm(x, residual, weight, eps, bufs.residual, bufs.y, bufs.y8, bufs.y_scale,
+                    bufs.rstd, stream)
+    return bufs
+
+
+class NormGrads:
+    """Gradients of the residual norm: ``dx`` (also the residual's, in the
+    activations' type), ``dresidual`` (the same values in the stream's type) and
+    ``dw`` float32, with the call's workspace."""
+
+    def __init__(self, T, D, dtype, residual_dtype, device):
+        self.dx = torch.empty((T, D), dtype=dtype, device=device)
+        self.dresidual = (self.dx if residual_dtype == dtype else
+                          torch.empty((T, D), dtype=residual_dtype, device=device))
+        self.dw = torch.empty((D,), dtype=torch.float32, device=device)
+        n = max(16, rom_add_rmsnorm_bwd_workspace_size(T, D))
+        self.ws = torch.empty((n,), dtype=torch.uint8, device=device)
+
+
+def add_rmsnorm_backward(dy, norm, weight, dresidual=None, bufs=None, stream=None):
+    """Backward of add_rmsnorm (``norm``: its NormBuffers): dy [T, Dm] is the
+    gradient of y, ``dresidual`` that of the new residual stream from the layers
+    after it (or None). Returns NormGrads."""
+    T, D = dy.shape
+    if bufs is None:
+        with _scope(dy, stream):
+            bufs = NormGrads(T, D, dy.dtype, norm.residual.dtype, dy.device)
+    rom_add_rmsnorm_bwd(dy, dresidual, norm.residual, weight, norm.rstd, bufs.dx,
+                        None if bufs.dresidual is bufs.dx else bufs.dresidual, bufs.dw, bufs.ws,
+                        stream)
+    return bufs
+
+
+class Q8BlockBuffers:
+    """Buffers of one 8-bit block forward; ``routing`` is a RoutingBuffers whose
+    x_sorted holds e4m3 rows, with their scales in ``x_scale_sorted``."""
+
+    def __init__(self, T, Dm, De, E, k, device):
+        R, e4, f32, bf = T * k, torch.float8_e4m3fn, torch.float32, torch.bfloat16
+        n = max(R, 1)
+        self.x8 = torch.empty((T, Dm), dtype=e4, device=device)
+        self.x_scale = torch.empty((T,), dtype=f32, device=device)
+        self.routing = RoutingBuffers(T, Dm, E, k, e4, device)
+        self.x_scale_sorted = torch.empty((n,), dtype=f32, device=device)
+        self.uz = torch.empty((2, R, De), dtype=f32, device=device) if k > 1 else None
+        self.h_sorted = torch.empty((R, De), dtype=bf, device=device)
+        self.h8 = torch.empty((R, De), dtype=e4, device=device)
+        self.h_scale = torch.empty((R,), dtype=f32, device=device)
+        self.o_slots = torch.empty((R, Dm), dtype=f32, device=device) if k > 1 else None
+        self.out = torch.empty((T, Dm), dtype=bf, device=device)
+
+
+def block_forward_q8(x, w_r, bias, w_conv, w_gate, w_out, k, renorm=False, x8=None, x_scale=None,
+                     bufs=None, stream=None):
+    """RoM block forward with the expert projections in 8 bits (Q8Weights).
+
+    x [T, Dm] bf16 is what the router reads; the experts read its 8-bit rows
+    ``x8``, ``x_scale`` (add_rmsnorm(..., q8=True) writes them beside x), made
+    here when not given. The gated rows h are rounded to bf16 and then to
+    8-bit rows for the Out projection. Returns the Q8BlockBuffers (O in
+    ``.out``)."""
+    T, Dm = x.shape
+    E, De = w_conv.E, w_conv.N
+    _t(x, "x", _BF16, T, w_conv.K)
+    _t(w_r, "w_r", _F32, Dm, E)
+    if bias is not None:
+        _t(bias, "bias", _F32, E)
+    if (x8 is None) != (x_scale is None):
+        raise RomError("x8 and x_scale come together")
+    if w_gate.q.shape != w_conv.q.shape or w_out.q.shape != (E, Dm, De):
+        raise RomError("the 8-bit weights' sizes do not fit together")
+    if Dm % 128 or De % 128:
+        raise RomError(f"d_model and d_inner must be multiples of 128, got {Dm} and {De}")
+    with _scope(x, stream):
+        if bufs is None:
+            bufs = Q8BlockBuffers(T, Dm, De, E, k, x.device)
+        if x8 is None:
+            x8, x_scale = bufs.x8, bufs.x_scale
+            rom_quant_rows(x, x8, x_scale, stream)
+        rb = bufs.routing
+        R = T * k
+        rom_route(x, w_r, bias, k, renorm, rb.topk_idx, rb.topk_w, rb.counts, rb.ws, stream)
+        rom_dispatch_q8(x8, x_scale, E, k, rb.topk_idx, rb.ws, rb.offsets, rb.sorted_slot,
+                        rb.slot_pos, rb.x_sorted, bufs.x_scale_sorted, stream)
+        rom_expert_proj_q8(ROM_PROJ_CONV_GATE, rb.x_sorted[:R], bufs.x_scale_sorted[:R], w_conv.q,
+                           w_conv.scale, w_gate.q, w_gate.scale, k, rb.offsets, rb.sorted_slot,
+                           rb.topk_w, bufs.h_sorted if k == 1 else bufs.uz, stream)
+        if k > 1:
+            rom_combine(ROM_COMBINE_GATE, ROM_BF16, bufs.uz, T, k, De, rb.slot_pos, bufs.h_sorted,
+                        stream)
+        rom_quant_rows(bufs.h_sorted, bufs.h8, bufs.h_scale, stream)
+        rom_expert_proj_q8(ROM_PROJ_OUT, bufs.h8, bufs.h_scale, w_out.q, w_out.scale, None, None, k,
+                           rb.offsets, rb.sorted_slot, rb.topk_w,
+                           bufs.out if k == 1 else bufs.o_slots, stream)
+        if k > 1:
+            rom_combine(ROM_COMBINE_SUM, ROM_BF16, bufs.o_slots, T, k, Dm, None, bufs.out, stream)
+    return bufs
+
+
+class W4BlockBuffers:
+    """Buffers of one block forward on 4-bit weights."""
+
+    def __init__(self, T, Dm, De, k, device):
+        R, f32, bf = T * k, torch.float32, torch.bfloat16
+        self.topk_idx = torch.empty((T, k), dtype=torch.int32, device=device)
+        self.topk_w = torch.empty((T, k), dtype=f32, device=device)
+        self.uz = torch.empty((2, R, De), dtype=f32, device=device)
+        self.h = torch.empty((T, De), dtype=bf, device=device)
+        self.o_slots = torch.empty((R, Dm), dtype=f32, device=device) if k > 1 else None
+        self.out = torch.empty((T, Dm), dtype=bf, device=device)
+
+
+def block_forward_w4(x, w_r, bias, w_conv, w_gate, w_out, k, renorm=False, bufs=None, stream=None):
+    """RoM block forward of a decode batch on 4-bit expert weights (W4Weights):
+    route, Conv+Gate, gate combine, Out, (sum), all in token order without a
+    dispatch. Any T, 64 tokens at a time; meant for few. x [T, Dm] bf16.
+    Returns the W4BlockBuffers (O in ``.out``)."""
+    T, Dm = x.shape
+    _t(x, "x", _BF16, T, w_conv.K)
+    _t(w_r, "w_r", _F32, Dm, w_conv.E)
+    if bias is not None:
+        _t(bias, "bias", _F32, w_conv.E)
+    if w_out.K != w_conv.N or w_out.N != Dm or w_gate.q.shape != w_conv.q.shape:
+        raise RomError("the 4-bit weights' sizes do not fit together")
+    De = w_conv.N
+    with _scope(x, stream):
+        if bufs is None:
+            bufs = W4BlockBuffers(T, Dm, De, k, x.device)
+        rom_route(x, w_r, bias, k, renorm, bufs.topk_idx, bufs.topk_w, None, None, stream)
+        _w4_tokens(ROM_PROJ_CONV_GATE_SLOTS, x, w_conv, w_gate, k, bufs.topk_idx, bufs.topk_w,
+                   bufs.uz, stream)
+        rom_combine(ROM_COMBINE_GATE, ROM_BF16, bufs.uz, T, k, De, None, bufs.h, stream)
+        _w4_tokens(ROM_PROJ_OUT, bufs.h, w_out, None, k, bufs.topk_idx, bufs.topk_w,
+                   bufs.out if k == 1 else bufs.o_slots, stream)
+        if k > 1:
+            rom_combine(ROM_COMBINE_SUM, ROM_BF16, bufs.o_slots, T, k, Dm, None, bufs.out, stream)
+    return bufs
+
+
+class ResidualBlock:
+    """One pre-norm block: ``norm`` (NormBuffers) and ``block`` (the block's
+    buffers); ``out`` is the block's output, ``residual`` the residual stream
+    that the next block's norm adds it to."""
+
+    def __init__(self, norm, block):
+        self.norm, self.block = norm, block
+        self.out, self.residual = block.out, norm.residual
+
+
+def residual_block_forward(x, residual, norm_w, w_r, bias, w_conv, w_gate, w_out, k, renorm=False,
+                           eps=1e-5, residual_dtype=torch.float32, norm_bufs=None, bufs=None,
+                           stream=None, keep_uz=False):
+    """Residual addition, norm and RoM block: block(norm(x + residual)).
+
+    x [T, Dm]: the previous block's output; residual [T, Dm] or None (first
+    block). The weights' type chooses the block: tensors (block_forward, bf16
+    or float32), Q8Weights (block_forward_q8, the norm writing the 8-bit rows)
+    or W4Weights (block_forward_w4). Returns a ResidualBlock."""
+    q8 = isinstance(w_conv, Q8Weights)
+    norm = add_rmsnorm(x, residual, norm_w, eps, q8, residual_dtype, norm_bufs, stream)
+    args = (norm.y, w_r, bias, w_conv, w_gate, w_out, k, renorm)
+    if q8:
+        block = block_forward_q8(*args, x8=norm.y8, x_scale=norm.y_scale, bufs=bufs, stream=stream)
+    elif isinstance(w_conv, W4Weights):
+        block = block_forward_w4(*args, bufs=bufs, stream=stream)
+    else:
+        with _scope(x, stream):
+            block = block_forward(*args, bufs=bufs, stream=stream, keep_uz=keep_uz)
+    return ResidualBlock(norm, block)
+
+
+def residual_block_backward(fwd, dout, norm_w, w_r, w_conv, w_gate, w_out, renorm=True, bias=None,
+                            dresidual=None, bufs=None, norm_bufs=None, stream=None,
+                            grad_sync=None):
+    """Backward of residual_block_forward on bf16 weights: dout [T, Dm] is the
+    gradient of the block's output, ``dresidual`` that of the residual stream
+    from the layers after it (or None). Returns (BackwardBuffers, NormGrads):
+    the expert and router gradients, and dx / dresidual of the block's inputs
+    with the norm weight's dw. With ``grad_sync`` the norm weight's gradient is
+    summed over the ranks too."""
+    with _scope(dout, stream):
+        bwd = block_backward(fwd.block, dout, w_r, w_conv, w_gate, w_out, renorm, bufs, stream,
+                             x=fwd.norm.y, bias=bias, grad_sync=grad_sync)
+        grads = add_rmsnorm_backward(bwd.dx, fwd.norm, norm_w, dresidual, norm_bufs, stream)
+        if grad_sync is not None:
+            grad_sync.start(grads.dw)
+            grad_sync.finish()
+    return bwd, grads
 
 
 # ------------------------------------------------------------------ projection variants
