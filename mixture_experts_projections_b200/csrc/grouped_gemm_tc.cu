@@ -988,6 +988,23 @@ cudaError_t launch_grouped(int mode, const void* a_sorted, const float* a_scale,
 
 }  // namespace
 
+bool make_tile_map(CUtensorMap* m, const void* base, int bytes, int64_t kb, int64_t tiles,
+                   int box_kb, int box_tiles) {
+  auto fn = encode_fn();
+  if (!fn) return false;
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(bytes / 4), static_cast<cuuint64_t>(kb),
+                              static_cast<cuuint64_t>(tiles)};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(bytes),
+                                 static_cast<cuuint64_t>(bytes) * static_cast<cuuint64_t>(kb)};
+  const cuuint32_t box[3] = {static_cast<cuuint32_t>(bytes / 4), static_cast<cuuint32_t>(box_kb),
+                             static_cast<cuuint32_t>(box_tiles)};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT32, 3, const_cast<void*>(base), dims, strides, box,
+            estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 cudaError_t launch_tc_grouped_gemm(int mode, const void* a_sorted, int64_t R, int K,
                                    const void* w0, const void* w1, int N, int E, int k,
                                    const int32_t* offsets, const int32_t* sorted_slot,

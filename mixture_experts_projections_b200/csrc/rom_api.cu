@@ -590,7 +590,8 @@ int rom_expert_proj_w4(int proj, const void* x, int64_t T, int K, const void* q0
       k > rom::kMaxTopK || (group != 32 && group != 64 && group != 128))
     return ROM_ERR_INVALID_ARG;
   if (gate != (q1 != nullptr) || gate != (s1 != nullptr)) return ROM_ERR_INVALID_ARG;
-  if (T > 64 || K % 8 != 0 || N > (1 << 30) || K > (1 << 30)) return ROM_ERR_UNSUPPORTED;
+  if (T > 64 || K % 8 != 0 || K > (1 << 24) || static_cast<int64_t>(E) * N > (1 << 30))
+    return ROM_ERR_UNSUPPORTED;
   if (T == 0) return ROM_OK;
   if (!x || !q0 || !s0 || !topk_idx || !out || (!gate && !slots && !topk_w))
     return ROM_ERR_INVALID_ARG;

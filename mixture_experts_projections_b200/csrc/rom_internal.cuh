@@ -1,6 +1,7 @@
 // Internal declarations shared by the translation units of librom.so.
 #pragma once
 
+#include <cuda.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -126,6 +127,12 @@ cudaError_t launch_add_rmsnorm_bwd(const void* dy, bool x_bf16, const void* dres
                                    cudaStream_t stream);
 cudaError_t launch_quant_rows(const void* x, bool x_bf16, int64_t rows, int D, void* q,
                               float* scale, cudaStream_t stream);
+
+// Tensor map over tiles of `bytes` (a multiple of 16, at most 1 KB) contiguous
+// bytes, [tiles][kb] of them: a box is box_kb positions of box_tiles tiles, zeros
+// outside (grouped_gemm_tc.cu).
+bool make_tile_map(CUtensorMap* m, const void* base, int bytes, int64_t kb, int64_t tiles,
+                   int box_kb, int box_tiles);
 
 // ---- 4-bit weights (w4_proj.cu); q1/s1: a second matrix (Conv+Gate), else null
 cudaError_t launch_w4_proj(const void* x, int T, int K, const void* q0, const void* s0,

@@ -6,14 +6,17 @@
 //   out[slot]  = r_slot * sum_c x[token][c] w[e_slot][:, c]
 //
 // What bounds it: the bytes of the selected experts' weights (half a byte per
-// weight, a quarter of bf16), so only experts that some token selected are
-// read, once for up to 32 of their tokens. The matrix instruction is the
-// warp-level m16n8k16, not tcgen05: its A operand (16 weight rows) comes from
-// registers, so a code goes from the loaded word to the tensor core without a
-// pass through shared memory, which for 2 bytes per weight would cost as much
-// time as reading the 4-bit weights from HBM. The codes are integers -8 .. 7,
-// exact in bf16; products with bf16 activations are exact in float32, sums are
-// float32, and a group's sum is multiplied by its scale in float32.
+// weight, a quarter of bf16) for few tokens, the instructions and shared-memory
+// reads of the products for many. Only experts that some token selected are
+// read, once for up to 24 of their tokens. The matrix instruction is the
+// warp-level m16n8k16: its A operand (16 weight rows) comes from registers, so a
+// code goes from the loaded word to the tensor core without a pass through
+// shared memory. tcgen05 measured slower here: with the weights in TMEM as A
+// (M = 128) an MMA of 16 or 32 tokens takes 60 cycles to issue, 8 per 128 x 128
+// block, and every unit of 128 rows waits for its accumulators (63 us for 64
+// tokens over 4 experts of 10240 x 4096 against 36). The codes are integers
+// -8 .. 7, exact in bf16; products with bf16 activations are exact in float32,
+// sums are float32, and a group's sum is multiplied by its scale in float32.
 //
 // Storage, a 1 KB tile per 16 rows x 128 columns, [E][N/16][K/128] tiles (N and
 // K rounded up; codes 8 and scales 0 there): byte h*512 + (g*4 + t)*16 + b holds
@@ -23,9 +26,12 @@
 // columns, nibbles p and p + 4 lie in one register's two halves after a shift
 // and a mask, and the B operand of a step is 8 contiguous bytes of the token's
 // row. A warp's loads are whole contiguous kilobytes.
+#include <cuda.h>
 #include <cuda_bf16.h>
 
 #include <algorithm>
+#include <atomic>
+#include <cmath>
 
 #include "rom_internal.cuh"
 #include "sm100_ptx.cuh"
@@ -33,23 +39,21 @@
 namespace rom {
 namespace {
 
-constexpr int kW4Warps = 8;                  // 16 weight rows each
-constexpr int kW4Threads = kW4Warps * 32;
-constexpr int kW4Rows = kW4Warps * 16;       // weight rows per CTA
+constexpr int kW4MaxWarps = 9;               // consumer warps of a CTA, 16 weight rows each
+constexpr int kW4MinWarps = 4;
 constexpr int kW4Stage = 2;                  // 128-column blocks per ring stage
 constexpr int kW4Cols = kW4Stage * 128;
-// Bytes of a token's row in a stage: 256 columns and a pad that puts the rows
-// of a quad column 32 bytes apart modulo 128 (conflict-free 8-byte reads).
+// Bytes of a token's row in a stage: its columns and a pad that puts the rows
+// 32 bytes apart modulo 128 (conflict-free 8-byte reads of the B operand).
 constexpr int kW4RowBytes = kW4Cols * 2 + 32;
-constexpr int kW4ScaleBytes = 128;           // per warp and block: 16 rows, up to 4 groups
-constexpr int kW4WarpBytes = kW4Stage * (1024 + kW4ScaleBytes);
-constexpr int kW4RedPitch = kW4Rows + 4;
+constexpr int kW4WarpBytes = kW4Stage * (1024 + 128);  // a warp's codes and scales
 constexpr int kW4MaxTokens = 64;
+constexpr int kW4MaxSlots = kW4MaxTokens * kMaxTopK;
+constexpr int kW4MaxStages = 6;
+constexpr int kW4MostSmem = 110 * 1024;   // of each of two CTAs on an SM
 
 struct W4Params {
   const __nv_bfloat16* x;
-  const uint8_t* q[2];
-  const __nv_bfloat16* s[2];
   const int32_t* topk_idx;
   const float* topk_w;  // null: unweighted
   void* out;
@@ -57,6 +61,7 @@ struct W4Params {
   int nt, kb;           // 16-row tiles, 128-column blocks
   int splits;           // CTAs of a cluster that share a row block's columns
   int max_active;       // upper bound of the experts in use
+  int stages;           // of the ring
   int to_token;         // bf16 rows in token order (k == 1), else float32 slot rows
   int* status;
 };
@@ -66,29 +71,35 @@ __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool f
                "r"(full ? 16 : 0)
                : "memory");
 }
-__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;"); }
-template <int N>
-__device__ __forceinline__ void cp_async_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+// One arrival on *bar (counted in its phase) once this thread's cp.async so far
+// have landed.
+__device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar))
+               : "memory");
 }
 
+// d += a b^T, and d = a b^T (16 x 8 x 16).
 __device__ __forceinline__ void mma_16816(float (&d)[4], const uint32_t (&a)[4], uint2 b) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
       "{%8, %9}, {%0, %1, %2, %3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b.x), "r"(b.y));
+}
+__device__ __forceinline__ void mma_16816_first(float (&d)[4], const uint32_t (&a)[4], uint2 b) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+      "{%8, %9}, {%10, %10, %10, %10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b.x), "r"(b.y), "f"(0.f));
 }
 
 // Two codes of a word (bits SH .. SH + 3 and SH + 16 .. SH + 19) as bf16 q - 8:
 // the bits of 128 + q (q < 16 sits in the mantissa's last 4 bits), less 136.
 template <int SH>
 __device__ __forceinline__ uint32_t codes(uint32_t w) {
-  const uint32_t v = ((w >> SH) & 0x000f000fu) | 0x43004300u;
-  const uint32_t c = 0x43084308u;
-  const __nv_bfloat162 d = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&v),
-                                   *reinterpret_cast<const __nv_bfloat162*>(&c));
-  return *reinterpret_cast<const uint32_t*>(&d);
+  uint32_t v, d;
+  asm("lop3.b32 %0, %1, %2, %3, 0xea;" : "=r"(v) : "r"(w >> SH), "r"(0x000f000fu), "r"(0x43004300u));
+  asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(v), "r"(0x3f803f80u), "r"(0xc308c308u));
+  return d;
 }
 
 __device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
@@ -98,29 +109,83 @@ __device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
 }
 
 struct W4Ctl {
+  uint64_t full[kW4MaxStages], empty[kW4MaxStages];
   uint32_t mask[2];  // experts in use
-  int count;
-  int slot[kW4MaxTokens * kMaxTopK];  // this expert's slots, in order
+  int abort;
+  int group_count[kW4MaxSlots / 32];  // of this expert's slots, per 32 slots
+  int16_t slot[kW4MaxSlots];          // this expert's slots, in order,
+  uint8_t tok[kW4MaxSlots];           // their tokens
+  float weight[kW4MaxSlots];          // and their routing weights (or 1)
 };
 
-template <int NB, int STAGES>
-constexpr size_t w4_smem_bytes() {
-  const size_t ring = static_cast<size_t>(STAGES) * (kW4Warps * kW4WarpBytes + NB * 8 * kW4RowBytes);
-  const size_t red = static_cast<size_t>(NB) * 8 * kW4RedPitch * 4;
-  return (ring > red ? ring : red) + sizeof(W4Ctl);
+// Ring, then the control block.
+template <int NB>
+__host__ __device__ constexpr int w4_stage_bytes(int warps) {
+  return warps * kW4WarpBytes + NB * 8 * kW4RowBytes;
 }
 
-// One CTA: 128 weight rows of one expert (and of one of up to two matrices)
-// times the expert's tokens, over its part of the columns. NB: 8-token blocks
-// held at a time; an expert with more tokens is passed over again. GS: steps of
-// 16 columns that share a scale (group / 16).
-template <int NB, int STAGES, int GS>
-__global__ void __launch_bounds__(kW4Threads, 2) w4_proj_kernel(const W4Params p) {
+// One 16 x 128 tile times NBL blocks of 8 tokens: acc += scale * (codes * x),
+// two steps of 16 columns at a time (one word of each row's codes), the chains
+// of the token blocks side by side. xs: this lane's first bytes of the first
+// block's x.
+template <int NBL, int GS, int NB>
+__device__ __forceinline__ void w4_tile(const uint4 qa, const uint4 qb, const __nv_bfloat16* sc,
+                                        int g, const uint8_t* xs, float (&acc)[NB][4]) {
+  constexpr int kGroups = 8 / GS;
+  const uint32_t wa[4] = {qa.x, qa.y, qa.z, qa.w}, wb[4] = {qb.x, qb.y, qb.z, qb.w};
+  float d[NBL][4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t a0[4] = {codes<0>(wa[i]), codes<0>(wb[i]), codes<4>(wa[i]), codes<4>(wb[i])};
+    const uint32_t a1[4] = {codes<8>(wa[i]), codes<8>(wb[i]), codes<12>(wa[i]), codes<12>(wb[i])};
+#pragma unroll
+    for (int nb = 0; nb < NBL; ++nb) {
+      const uint8_t* xb = xs + nb * 8 * kW4RowBytes + i * 64;
+      if (2 * i % GS == 0)
+        mma_16816_first(d[nb], a0, *reinterpret_cast<const uint2*>(xb));
+      else
+        mma_16816(d[nb], a0, *reinterpret_cast<const uint2*>(xb));
+    }
+#pragma unroll
+    for (int nb = 0; nb < NBL; ++nb)
+      mma_16816(d[nb], a1,
+                *reinterpret_cast<const uint2*>(xs + nb * 8 * kW4RowBytes + i * 64 + 32));
+    if ((2 * i + 2) % GS == 0) {
+      const int gr = (2 * i) / GS;
+      const float lo = __bfloat162float(sc[g * kGroups + gr]);
+      const float hi = __bfloat162float(sc[(g + 8) * kGroups + gr]);
+#pragma unroll
+      for (int nb = 0; nb < NBL; ++nb) {
+        acc[nb][0] = fmaf(lo, d[nb][0], acc[nb][0]);
+        acc[nb][1] = fmaf(lo, d[nb][1], acc[nb][1]);
+        acc[nb][2] = fmaf(hi, d[nb][2], acc[nb][2]);
+        acc[nb][3] = fmaf(hi, d[nb][3], acc[nb][3]);
+      }
+    }
+  }
+}
+
+// Tensor maps of the codes (1 KB tiles) and scales of up to two matrices.
+struct W4Maps {
+  CUtensorMap q[2], s[2];
+};
+
+// One CTA: 16 weight rows per consumer warp of one expert (and of one of up to
+// two matrices) times the expert's tokens, over its part of the columns. The
+// last warp feeds the ring, so the consumers spend no instruction on addresses:
+// the codes and the scales of all warps' tiles come in one TMA copy each (a
+// bulk copy per tile and row cost 90 cycles apiece to issue, 3600 a stage), the
+// tokens' rows by 16-byte copies that arrive on the stage's barrier. NB: 8-token
+// blocks held at a time; an expert with more tokens is passed over again. GS:
+// steps of 16 columns that share a scale (group / 16). Every wait is bounded.
+template <int NB, int GS>
+__global__ void __maxnreg__(96)
+    w4_proj_kernel(const __grid_constant__ W4Maps maps, const W4Params p) {
   extern __shared__ __align__(128) uint8_t smem[];
   constexpr int kTok = NB * 8;
-  constexpr int kStageBytes = kW4Warps * kW4WarpBytes + kTok * kW4RowBytes;
-  constexpr size_t kCtlAt = w4_smem_bytes<NB, STAGES>() - sizeof(W4Ctl);
-  W4Ctl& ctl = *reinterpret_cast<W4Ctl*>(smem + kCtlAt);
+  const int warps = (blockDim.x >> 5) - 1;  // consumers
+  const int stage_bytes = w4_stage_bytes<NB>(warps);
+  W4Ctl& ctl = *reinterpret_cast<W4Ctl*>(smem + p.stages * stage_bytes);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
   const int rank = p.splits > 1 ? static_cast<int>(cluster_ctarank()) : 0;
   const int row_blk = blockIdx.x / p.splits;
@@ -129,14 +194,35 @@ __global__ void __launch_bounds__(kW4Threads, 2) w4_proj_kernel(const W4Params p
   const int nslots = p.T * p.k;
 
   if (tid < 2) ctl.mask[tid] = 0;
+  if (tid == 0) {
+    for (int i = 0; i < p.stages; ++i) {
+      mbar_init(&ctl.full[i], 1 + 32);  // the TMA copies, the producer's lanes
+      mbar_init(&ctl.empty[i], warps);
+    }
+    ctl.abort = 0;
+    fence_barrier_init();
+  }
   pdl_wait();  // the router's outputs and x are complete from here
   __syncthreads();
-  for (int i = tid; i < nslots; i += kW4Threads) {
-    const int e = p.topk_idx[i];
-    if (e >= 0 && e < p.E)
-      atomicOr(&ctl.mask[e >> 5], 1u << (e & 31));
-    else if (p.status)
-      atomicExch(p.status, kStatusRouting);
+  // Every thread keeps its slots' experts; the slots of 32 consecutive threads
+  // are one group.
+  constexpr int kMine = (kW4MaxSlots + (kW4MinWarps + 1) * 32 - 1) / ((kW4MinWarps + 1) * 32);
+  int my_e[kMine];
+  float my_w[kMine];
+#pragma unroll
+  for (int i = 0; i < kMine; ++i) {
+    const int sl = i * blockDim.x + tid;
+    my_e[i] = -1;
+    if (sl < nslots) {
+      const int v = p.topk_idx[sl];
+      my_w[i] = p.topk_w ? p.topk_w[sl] : 1.f;
+      if (v >= 0 && v < p.E) {
+        my_e[i] = v;
+        atomicOr(&ctl.mask[v >> 5], 1u << (v & 31));
+      } else if (p.status) {
+        atomicExch(p.status, kStatusRouting);
+      }
+    }
   }
   __syncthreads();
   // the nth expert in use; every CTA of a cluster leaves or stays together
@@ -145,32 +231,43 @@ __global__ void __launch_bounds__(kW4Threads, 2) w4_proj_kernel(const W4Params p
   uint64_t rest = mask;
   for (int i = 0; i < nth; ++i) rest &= rest - 1;
   const int e = __ffsll(static_cast<long long>(rest)) - 1;
-  if (warp == 0) {
-    int n = 0;
-    for (int i = 0; i < nslots; i += 32) {
-      const bool mine = i + lane < nslots && p.topk_idx[i + lane] == e;
-      const unsigned b = __ballot_sync(0xffffffffu, mine);
-      if (mine) ctl.slot[n + __popc(b & ((1u << lane) - 1u))] = i + lane;
-      n += __popc(b);
+  const int groups = (nslots + 31) / 32;
+#pragma unroll
+  for (int i = 0; i < kMine; ++i) {
+    const int grp = i * (warps + 1) + warp;
+    if (grp < groups) {
+      const unsigned b = __ballot_sync(0xffffffffu, my_e[i] == e);
+      if (lane == 0) ctl.group_count[grp] = __popc(b);
     }
-    if (lane == 0) ctl.count = n;
   }
   __syncthreads();
-  const int count = ctl.count;
+  int count = 0;
+  for (int grp = 0; grp < groups; ++grp) {
+    const int n = ctl.group_count[grp];
+#pragma unroll
+    for (int i = 0; i < kMine; ++i) {
+      if (grp == i * (warps + 1) + warp) {  // warp-uniform
+        const unsigned b = __ballot_sync(0xffffffffu, my_e[i] == e);
+        if (my_e[i] == e) {
+          const int at = count + __popc(b & ((1u << lane) - 1u)), sl = grp * 32 + lane;
+          ctl.slot[at] = static_cast<int16_t>(sl);
+          ctl.tok[at] = static_cast<uint8_t>(sl / p.k);
+          ctl.weight[at] = my_w[i];
+        }
+      }
+    }
+    count += n;
+  }
+  __syncthreads();
+  volatile int* abort_flag = &ctl.abort;
 
-  const int tile = row_blk * kW4Warps + warp;
-  const bool has_tile = tile < p.nt;
-  const int64_t tile0 = (static_cast<int64_t>(e) * p.nt + (has_tile ? tile : 0)) * p.kb;
-  const uint8_t* qw = (mat ? p.q[1] : p.q[0]) + tile0 * 1024 + lane * 16;
-  constexpr int kGroups = 8 / GS;                 // scales per row and block
-  constexpr int kScaleLanes = 2 * kGroups;        // 16-byte pieces of a block's scales
-  const uint8_t* sw =
-      reinterpret_cast<const uint8_t*>(mat ? p.s[1] : p.s[0]) + tile0 * (kScaleLanes * 16) + lane * 16;
+  constexpr int kScaleBytes = 32 * (8 / GS);  // of a 16 x 128 tile
   // this CTA's blocks of 128 columns
   const int b0 = static_cast<int>(static_cast<int64_t>(p.kb) * rank / p.splits);
   const int b1 = static_cast<int>(static_cast<int64_t>(p.kb) * (rank + 1) / p.splits);
-  const int iters = (b1 - b0 + kW4Stage - 1) / kW4Stage;
-  const uint32_t smem0 = smem_u32(smem);
+  const int tiles = min(warps, p.nt - row_blk * warps);  // warps with rows
+  int stage = 0;
+  uint32_t phase = 0;
 
   for (int p0 = 0; p0 < count; p0 += kTok) {
     const int n_tok = min(kTok, count - p0);
@@ -181,130 +278,128 @@ __global__ void __launch_bounds__(kW4Threads, 2) w4_proj_kernel(const W4Params p
 #pragma unroll
       for (int j = 0; j < 4; ++j) acc[nb][j] = 0.f;
 
-    auto issue = [&](int it) {
-      if (it < iters) {
-        const uint32_t st = smem0 + (it % STAGES) * kStageBytes;
-        const uint32_t ws = st + warp * kW4WarpBytes;
+    if (warp == warps) {
+      // ------------------------------------------------ producer
+      // (a last row block's missing tiles: the next expert's, or zeros, not used)
+      const int tile0 = e * p.nt + row_blk * warps;
+      const CUtensorMap* mq = &maps.q[mat];
+      const CUtensorMap* ms = &maps.s[mat];
+      uint32_t src[kTok];  // 16-byte pieces; lane l: columns 8 l .. + 7 of a stage
 #pragma unroll
-        for (int b = 0; b < kW4Stage; ++b) {
-          const int kb = b0 + it * kW4Stage + b;
-          if (has_tile && kb < b1) {
-            const uint8_t* src = qw + static_cast<int64_t>(kb) * 1024;
-            cp_async16(ws + b * 1024 + lane * 16, src, true);
-            cp_async16(ws + b * 1024 + 512 + lane * 16, src + 512, true);
-            if (lane < kScaleLanes)
-              cp_async16(ws + kW4Stage * 1024 + b * kW4ScaleBytes + lane * 16,
-                         sw + static_cast<int64_t>(kb) * (kScaleLanes * 16), true);
-          }
+      for (int r = 0; r < kTok; ++r)
+        src[r] = (r < n_tok ? ctl.tok[p0 + r] : 0u) * (static_cast<uint32_t>(p.K) / 8u) + lane;
+      const uint4* xsrc = reinterpret_cast<const uint4*>(p.x);
+      uint32_t issued = 0, last_par = 0;
+      for (int kb = b0; kb < b1; kb += kW4Stage) {
+        if (!__all_sync(0xffffffffu,
+                        mbar_wait(&ctl.empty[stage], phase ^ 1u, abort_flag, p.status)))
+          break;
+        uint8_t* st = smem + stage * stage_bytes;
+        if (lane == 0) {
+          mbar_arrive_expect_tx(&ctl.full[stage], warps * kW4Stage * (1024 + kScaleBytes));
+          tma_load_3d(st, mq, &ctl.full[stage], 0, kb, tile0);
+          tma_load_3d(st + warps * kW4Stage * 1024, ms, &ctl.full[stage], 0, kb, tile0);
         }
-        const uint32_t xs = st + kW4Warps * kW4WarpBytes;
-        const int c0 = (b0 + it * kW4Stage) * 128;
-        const int cend = min(p.K, b1 * 128);
-        for (int i = tid; i < n_blk * 8 * (kW4Cols / 8); i += kW4Threads) {
-          const int r = i / (kW4Cols / 8), c = (i % (kW4Cols / 8)) * 8;
-          const bool in = r < n_tok && c0 + c < cend;
-          const int64_t tok = in ? ctl.slot[p0 + r] / p.k : 0;
-          cp_async16(xs + r * kW4RowBytes + c * 2, p.x + tok * p.K + (in ? c0 + c : 0), in);
+        const uint32_t xd = smem_u32(st + warps * kW4WarpBytes + lane * 16);
+        const int c = kb * 128 + lane * 8;
+        const bool in = c < min(p.K, b1 * 128);  // other columns: zeros
+#pragma unroll
+        for (int r = 0; r < kTok; ++r)
+          if (r < n_tok) cp_async16(xd + r * kW4RowBytes, xsrc + (in ? src[r] + kb * 16 : 0u), in);
+        cp_async_arrive(&ctl.full[stage]);
+        issued |= 1u << stage;
+        last_par = (last_par & ~(1u << stage)) | (phase << stage);
+        if (++stage == p.stages) {
+          stage = 0;
+          phase ^= 1u;
         }
       }
-      cp_async_commit();
-    };
-
+      // every copy has landed before the ring is used for the sums
+      int never = 0;
+      for (int i = 0; i < p.stages; ++i)
+        if ((issued >> i) & 1u) mbar_wait(&ctl.full[i], (last_par >> i) & 1u, &never, p.status);
+    } else {
+      // ------------------------------------------------ consumers
+      for (int kb = b0; kb < b1; kb += kW4Stage) {
+        if (!mbar_wait(&ctl.full[stage], phase, abort_flag, p.status)) break;
+        const uint8_t* st = smem + stage * stage_bytes;
+        const uint8_t* ws = st + warp * (kW4Stage * 1024);
+        const uint8_t* ss = st + warps * (kW4Stage * 1024) + warp * (kW4Stage * kScaleBytes);
+        const uint8_t* xs = st + warps * kW4WarpBytes + g * kW4RowBytes + t * 8;
+        if (warp < tiles) {
 #pragma unroll
-    for (int it = 0; it < STAGES - 1; ++it) issue(it);
-    for (int it = 0; it < iters; ++it) {
-      cp_async_wait<STAGES - 2>();
-      __syncthreads();
-      issue(it + STAGES - 1);
-      const uint8_t* st = smem + (it % STAGES) * kStageBytes;
-      const uint8_t* ws = st + warp * kW4WarpBytes;
-      const uint8_t* xs = st + kW4Warps * kW4WarpBytes + g * kW4RowBytes + t * 8;
-#pragma unroll
-      for (int b = 0; b < kW4Stage; ++b) {
-        if (!has_tile || b0 + it * kW4Stage + b >= b1) continue;  // warp-uniform
-        const uint4 qa = *reinterpret_cast<const uint4*>(ws + b * 1024 + lane * 16);
-        const uint4 qb = *reinterpret_cast<const uint4*>(ws + b * 1024 + 512 + lane * 16);
-        const uint32_t wa[4] = {qa.x, qa.y, qa.z, qa.w}, wb[4] = {qb.x, qb.y, qb.z, qb.w};
-        uint32_t a[8][4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          a[2 * i][0] = codes<0>(wa[i]);
-          a[2 * i][1] = codes<0>(wb[i]);
-          a[2 * i][2] = codes<4>(wa[i]);
-          a[2 * i][3] = codes<4>(wb[i]);
-          a[2 * i + 1][0] = codes<8>(wa[i]);
-          a[2 * i + 1][1] = codes<8>(wb[i]);
-          a[2 * i + 1][2] = codes<12>(wa[i]);
-          a[2 * i + 1][3] = codes<12>(wb[i]);
-        }
-        const __nv_bfloat16* sc = reinterpret_cast<const __nv_bfloat16*>(
-            ws + kW4Stage * 1024 + b * kW4ScaleBytes);
-        float s_lo[kGroups], s_hi[kGroups];
-#pragma unroll
-        for (int i = 0; i < kGroups; ++i) {
-          s_lo[i] = __bfloat162float(sc[g * kGroups + i]);
-          s_hi[i] = __bfloat162float(sc[(g + 8) * kGroups + i]);
-        }
-#pragma unroll
-        for (int nb = 0; nb < NB; ++nb) {
-          if (nb < n_blk) {  // CTA-uniform
-            const uint8_t* xb = xs + nb * 8 * kW4RowBytes + b * 256;
-#pragma unroll
-            for (int i = 0; i < kGroups; ++i) {
-              float d[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-              for (int j = 0; j < GS; ++j)
-                mma_16816(d, a[i * GS + j],
-                          *reinterpret_cast<const uint2*>(xb + (i * GS + j) * 32));
-              acc[nb][0] = fmaf(s_lo[i], d[0], acc[nb][0]);
-              acc[nb][1] = fmaf(s_lo[i], d[1], acc[nb][1]);
-              acc[nb][2] = fmaf(s_hi[i], d[2], acc[nb][2]);
-              acc[nb][3] = fmaf(s_hi[i], d[3], acc[nb][3]);
-            }
+          for (int b = 0; b < kW4Stage; ++b) {
+            if (b > 0 && kb + b >= b1) break;
+            const uint4 qa = *reinterpret_cast<const uint4*>(ws + b * 1024 + lane * 16);
+            const uint4 qb = *reinterpret_cast<const uint4*>(ws + b * 1024 + 512 + lane * 16);
+            const __nv_bfloat16* sc =
+                reinterpret_cast<const __nv_bfloat16*>(ss + b * kScaleBytes);
+            if (NB == 1 || n_blk == 1)
+              w4_tile<1, GS>(qa, qb, sc, g, xs + b * 256, acc);
+            else if (NB == 2 || n_blk == 2)
+              w4_tile<NB < 2 ? 1 : 2, GS>(qa, qb, sc, g, xs + b * 256, acc);
+            else
+              w4_tile<NB < 3 ? 1 : 3, GS>(qa, qb, sc, g, xs + b * 256, acc);
           }
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ctl.empty[stage]);
+        if (++stage == p.stages) {
+          stage = 0;
+          phase ^= 1u;
         }
       }
     }
 
-    // The sums meet in shared memory as [token][row] (over the ring, which no
-    // copy still writes), are added over the cluster in rank order and stored
-    // row-contiguous.
-    cp_async_wait<0>();
+    // The sums meet in shared memory as [token][row] (over the ring, whose
+    // copies have all landed and been read), are added over the cluster in rank
+    // order and stored row-contiguous.
     __syncthreads();
     float* red = reinterpret_cast<float*>(smem);
+    const int pitch = warps * 16 + 4;
+    if (warp < warps) {
 #pragma unroll
-    for (int nb = 0; nb < NB; ++nb) {
-      if (nb < n_blk) {
-        float* r0 = red + (nb * 8 + 2 * t) * kW4RedPitch + warp * 16 + g;
-        r0[0] = acc[nb][0];
-        r0[kW4RedPitch] = acc[nb][1];
-        r0[8] = acc[nb][2];
-        r0[kW4RedPitch + 8] = acc[nb][3];
+      for (int nb = 0; nb < NB; ++nb) {
+        if (nb < n_blk) {
+          float* r0 = red + (nb * 8 + 2 * t) * pitch + warp * 16 + g;
+          r0[0] = acc[nb][0];
+          r0[pitch] = acc[nb][1];
+          r0[8] = acc[nb][2];
+          r0[pitch + 8] = acc[nb][3];
+        }
       }
     }
+    fence_async_shared();  // before the next pass's copies into the same bytes
+    __syncwarp();
     if (p.splits > 1)
       cluster_sync_all();
     else
       __syncthreads();
-    const int rows = kW4Rows / p.splits;  // this rank's share of the rows
-    for (int i = tid; i < n_tok * rows; i += kW4Threads) {
-      const int j = i / rows, r = rank * rows + (i - j * rows);
-      const int n = row_blk * kW4Rows + r;
-      if (n < p.N) {
-        float v = 0.f;
+    const int rows = warps * 16 / p.splits;  // this rank's share of the rows
+    const int row0 = rank * rows, n0 = row_blk * warps * 16 + row0;
+    const int n_rows = *abort_flag ? 0 : min(rows, p.N - n0);
+    for (int j = warp; j < n_tok; j += warps + 1) {
+      const float r = ctl.weight[p0 + j];
+      const int slot = ctl.slot[p0 + j];
+      const float* from = red + j * pitch + row0;
+      __nv_bfloat16* o16 = static_cast<__nv_bfloat16*>(p.out) + static_cast<int64_t>(slot) * p.N + n0;
+      float* o32 =
+          static_cast<float*>(p.out) + (static_cast<int64_t>(mat) * nslots + slot) * p.N + n0;
+#pragma unroll 4
+      for (int i = lane; i < n_rows; i += 32) {
+        float v;
         if (p.splits > 1) {
-          const uint32_t at = smem_u32(red + j * kW4RedPitch + r);
+          const uint32_t at = smem_u32(from + i);
+          v = 0.f;
           for (int c = 0; c < p.splits; ++c) v += ld_cluster_f32(mapa_shared(at, c));
         } else {
-          v = red[j * kW4RedPitch + r];
+          v = from[i];
         }
-        const int slot = ctl.slot[p0 + j];
-        if (p.topk_w) v *= p.topk_w[slot];
+        v *= r;
         if (p.to_token)
-          static_cast<__nv_bfloat16*>(p.out)[static_cast<int64_t>(slot) * p.N + n] =
-              __float2bfloat16_rn(v);
+          o16[i] = __float2bfloat16_rn(v);
         else
-          static_cast<float*>(p.out)[(static_cast<int64_t>(mat) * nslots + slot) * p.N + n] = v;
+          o32[i] = v;
       }
     }
     // no CTA reuses or leaves its shared memory while another reads it
@@ -313,17 +408,31 @@ __global__ void __launch_bounds__(kW4Threads, 2) w4_proj_kernel(const W4Params p
       cluster_sync_all();
     else
       __syncthreads();
+    if (*abort_flag && p.splits == 1) return;
   }
 }
 
-template <int NB, int STAGES, int GS>
-cudaError_t launch_w4(const W4Params& p, int mats, cudaStream_t stream) {
-  auto kern = w4_proj_kernel<NB, STAGES, GS>;
-  constexpr size_t smem = w4_smem_bytes<NB, STAGES>();
-  const cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               static_cast<int>(smem));
+template <int NB, int GS>
+cudaError_t launch_w4(W4Params p, const W4Maps& maps, int warps, int mats, cudaStream_t stream) {
+  auto kern = w4_proj_kernel<NB, GS>;
+  // Once per device: the most shared memory a launch asks for, and the largest
+  // carve-out, so that several CTAs fit an SM.
+  static std::atomic<uint64_t> ready{0};
+  int dev = 0;
+  cudaError_t err = cudaGetDevice(&dev);
   if (err != cudaSuccess) return err;
-  const int row_blks = (p.nt + kW4Warps - 1) / kW4Warps;
+  if (dev >= 64 || !((ready.load() >> dev) & 1u)) {
+    err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kW4MostSmem);
+    if (err != cudaSuccess) return err;
+    err = cudaFuncSetAttribute(kern, cudaFuncAttributePreferredSharedMemoryCarveout,
+                               cudaSharedmemCarveoutMaxShared);
+    if (err != cudaSuccess) return err;
+    if (dev < 64) ready.fetch_or(uint64_t(1) << dev);
+  }
+  const int row_blks = (p.nt + warps - 1) / warps;
+  const int stage = w4_stage_bytes<NB>(warps);
+  const int budget = kW4MostSmem - static_cast<int>(sizeof(W4Ctl));
+  p.stages = std::min(kW4MaxStages, budget / stage);
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
@@ -334,23 +443,24 @@ cudaError_t launch_w4(const W4Params& p, int mats, cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(row_blks * p.splits),
                      static_cast<unsigned>(p.max_active * mats), 1);
-  cfg.blockDim = dim3(kW4Threads, 1, 1);
-  cfg.dynamicSmemBytes = smem;
+  cfg.blockDim = dim3(static_cast<unsigned>((warps + 1) * 32), 1, 1);
+  cfg.dynamicSmemBytes = static_cast<size_t>(p.stages) * stage + sizeof(W4Ctl);
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = p.splits > 1 ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, kern, p);
+  return cudaLaunchKernelEx(&cfg, kern, maps, p);
 }
 
-template <int NB, int STAGES>
-cudaError_t launch_w4_group(const W4Params& p, int mats, int group, cudaStream_t stream) {
+template <int NB>
+cudaError_t launch_w4_group(const W4Params& p, const W4Maps& maps, int warps, int mats, int group,
+                            cudaStream_t stream) {
   switch (group) {
     case 32:
-      return launch_w4<NB, STAGES, 2>(p, mats, stream);
+      return launch_w4<NB, 2>(p, maps, warps, mats, stream);
     case 64:
-      return launch_w4<NB, STAGES, 4>(p, mats, stream);
+      return launch_w4<NB, 4>(p, maps, warps, mats, stream);
     default:
-      return launch_w4<NB, STAGES, 8>(p, mats, stream);
+      return launch_w4<NB, 8>(p, maps, warps, mats, stream);
   }
 }
 
@@ -438,10 +548,6 @@ cudaError_t launch_w4_proj(const void* x, int T, int K, const void* q0, const vo
                            int* status, cudaStream_t stream) {
   W4Params p{};
   p.x = static_cast<const __nv_bfloat16*>(x);
-  p.q[0] = static_cast<const uint8_t*>(q0);
-  p.q[1] = static_cast<const uint8_t*>(q1);
-  p.s[0] = static_cast<const __nv_bfloat16*>(s0);
-  p.s[1] = static_cast<const __nv_bfloat16*>(s1);
   p.topk_idx = topk_idx;
   p.topk_w = topk_w;
   p.out = out;
@@ -456,17 +562,44 @@ cudaError_t launch_w4_proj(const void* x, int T, int K, const void* q0, const vo
   p.status = status;
   p.max_active = std::min(E, T * k);
   const int mats = q1 ? 2 : 1;
-  // Few row blocks (few tokens or a small N): the CTAs of a cluster share a
-  // row block's columns, until there are about two CTAs per SM or a CTA is
-  // left with fewer than 4 blocks of 128 columns.
-  const int64_t units = static_cast<int64_t>((p.nt + kW4Warps - 1) / kW4Warps) * p.max_active * mats;
-  p.splits = 1;
-  while (p.splits < 8 && units * p.splits < 2 * static_cast<int64_t>(device_sm_count()) &&
-         p.kb / (p.splits * 2) >= 4)
-    p.splits *= 2;
-  if (T <= 8) return launch_w4_group<1, 4>(p, mats, group, stream);
-  if (T <= 16) return launch_w4_group<2, 4>(p, mats, group, stream);
-  return launch_w4_group<4, 3>(p, mats, group, stream);
+  // Shape of the work: CTAs of `warps` 16-row tiles, `splits` of them (a
+  // cluster) sharing the columns of one row block. The cost is an SM's: the
+  // tiles that its CTAs' warps go through, ceil(CTAs / SMs) * warps / splits,
+  // slower where few warps are resident (two CTAs fit) and where a third round
+  // starts late, plus the cluster's hand-over of its sums (1.5 tiles of 4096
+  // columns per split). Measured, us, at 4 experts of 10240 x 4096: one token 10.9 (9
+  // warps, 2 splits; 12.6 with 4 and 1, 14.0 with 9 and 4), 4 tokens 14.2 (9 and
+  // 2; 15.0 with 5 and 1), 64 tokens 36.3 (9 and 1; 44 with 5, 47 with 8).
+  const double used = E * (1.0 - std::pow(1.0 - static_cast<double>(k) / E, T));
+  const int sms = device_sm_count();
+  int warps = kW4MaxWarps;
+  double best = 1e30;
+  for (int s = 1; s <= 8 && (s == 1 || p.kb / s >= 4); s *= 2) {
+    for (int w = kW4MaxWarps; w >= kW4MinWarps; --w) {
+      const double rounds = std::ceil(std::ceil(((p.nt + w - 1) / w) * used * mats * s) / sms);
+      const double resident = std::min(rounds, 2.0) * w;
+      const double cost = rounds * w / s * (1.0 + 6.0 / resident) * (rounds > 2 ? 1.1 : 1.0) +
+                          (s > 1 ? 1.5 * s * 32.0 / p.kb : 0.0);
+      if (cost < best * 0.999) {
+        best = cost;
+        warps = w;
+        p.splits = s;
+      }
+    }
+  }
+  W4Maps maps;
+  const int64_t tiles = static_cast<int64_t>(E) * p.nt;
+  for (int i = 0; i < mats; ++i)
+    if (!make_tile_map(&maps.q[i], i ? q1 : q0, 1024, p.kb, tiles, kW4Stage, warps) ||
+        !make_tile_map(&maps.s[i], i ? s1 : s0, 32 * (128 / group), p.kb, tiles, kW4Stage, warps))
+      return cudaErrorInvalidValue;
+  if (mats == 1) {
+    maps.q[1] = maps.q[0];
+    maps.s[1] = maps.s[0];
+  }
+  if (T <= 8) return launch_w4_group<1>(p, maps, warps, mats, group, stream);
+  if (T <= 16) return launch_w4_group<2>(p, maps, warps, mats, group, stream);
+  return launch_w4_group<3>(p, maps, warps, mats, group, stream);
 }
 
 cudaError_t launch_quant_w4(const void* w, bool bf16, int E, int N, int K, int group, void* q,

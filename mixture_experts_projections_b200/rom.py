@@ -230,7 +230,7 @@ def _t(t, name, dtype, *shape):
     returns its address."""
     if t.dtype is not dtype or t.shape != shape:
         raise RomError(f"{name} must be {dtype} {list(shape)}, got {t.dtype} {list(t.shape)}")
-    if not t.is_cuda or not t.is_contiguous():
+    if not t.is_contiguous():
         raise RomError(f"{name} must be a contiguous CUDA tensor")
     return t.data_ptr()
 
@@ -242,20 +242,25 @@ def _call(fn, stream, tensors, *args):
     for t in tensors:
         if t is not None:
             i = t.get_device()
-            if index is None:
+            if i != index:
+                if i < 0:
+                    raise RomError(f"{fn}: its tensors must be contiguous CUDA tensors")
+                if index is not None:
+                    raise RomError(f"{fn}: tensors on different devices (cuda:{index}, cuda:{i})")
                 index = i
-            elif i != index:
-                raise RomError(f"{fn}: tensors on different devices (cuda:{index}, cuda:{i})")
     if stream is None:
-        stream = torch.cuda.current_stream(index)
-    elif stream.device.index != index:
+        # the handle alone: a Stream object costs 1.2 us of a 10 us call
+        handle = torch._C._cuda_getCurrentRawStream(index)
+    elif stream.device.index == index:
+        handle = stream.cuda_stream
+    else:
         raise RomError(f"{fn}: the stream is not one of cuda:{index}")
     lib = _lib or load_library()
     if torch.cuda.current_device() == index:
-        code = getattr(lib, fn)(*args, stream.cuda_stream)
+        code = getattr(lib, fn)(*args, handle)
     else:
         with torch.cuda.device(index):
-            code = getattr(lib, fn)(*args, stream.cuda_stream)
+            code = getattr(lib, fn)(*args, handle)
     if code != ROM_OK:
         _check(code, fn)
 

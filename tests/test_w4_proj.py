@@ -141,7 +141,8 @@ def test_expert_proj_w4_matches_the_products(T, K, N, E, k, group, pin):
     assert (got[2 * R] == 7).all()
     out = torch.full((R + 1, N), 7.0, device="cuda")
     rom.rom_expert_proj_w4(rom.ROM_PROJ_SLOTS, d[0], d[3], d[4], None, None, N, k, idxd, None, out[:R])
-    assert torch.equal(out[:R], uz[R:2 * R]) and (out[R] == 7).all()
+    # (not bit for bit: how the columns are shared out goes by the whole call)
+    assert ((out[:R].cpu().double() - v1).abs() <= acc_err(K, m1)).all() and (out[R] == 7).all()
     rr = torch.from_numpy(r).double().view(-1, 1)
     e = rr * (acc_err(K, m0) + U * v0.abs())
     if k == 1:
@@ -182,7 +183,8 @@ def test_expert_proj_w4_repeated_and_invalid_experts():
     assert rom.rom_get_status() == rom.ROM_ERR_ROUTING
     left = torch.zeros(T * k, dtype=torch.bool)
     left[[1, 21]] = True
-    assert (out2[left.cuda()] == 7).all() and torch.equal(out2[~left.cuda()], out[~left.cuda()])
+    assert (out2[left.cuda()] == 7).all()
+    assert ((out2.cpu().double() - v).abs() <= acc_err(K, m))[~left].all()
 
 
 @gpu
