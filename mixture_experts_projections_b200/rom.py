@@ -225,42 +225,51 @@ def rom_route_dispatch_noalloc(x, w_r, bias, k, renorm, topk_idx, topk_w, counts
 # current, and take the current stream of that device unless given one.
 
 
-def _t(t, name, dtype, *shape):
-    """Refuses a tensor of another type, shape or layout, or on the CPU;
+def _t(t, name, dtype, shape, dev):
+    """Refuses a tensor of another type, shape, layout or device than cuda:dev;
     returns its address."""
-    if t.dtype is not dtype or t.shape != shape:
-        raise RomError(f"{name} must be {dtype} {list(shape)}, got {t.dtype} {list(t.shape)}")
-    if not t.is_contiguous():
-        raise RomError(f"{name} must be a contiguous CUDA tensor")
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != dev or not t.is_contiguous():
+        if t.dtype is not dtype or t.shape != shape:
+            raise RomError(f"{name} must be {dtype} {list(shape)}, got {t.dtype} {list(t.shape)}")
+        if not t.is_cuda or not t.is_contiguous():
+            raise RomError(f"{name} must be a contiguous CUDA tensor")
+        raise RomError(f"{name} is on {t.device}, the call's first tensor on cuda:{dev}")
     return t.data_ptr()
 
 
-def _call(fn, stream, tensors, *args):
-    """Calls a library function with the stream as its last argument, on the
-    device of ``tensors`` (which must all be the same)."""
-    index = None
-    for t in tensors:
-        if t is not None:
-            i = t.get_device()
-            if i != index:
-                if i < 0:
-                    raise RomError(f"{fn}: its tensors must be contiguous CUDA tensors")
-                if index is not None:
-                    raise RomError(f"{fn}: tensors on different devices (cuda:{index}, cuda:{i})")
-                index = i
+def _device(t, name):
+    """The index of the CUDA device that a call runs on: that of its first tensor."""
+    dev = t.get_device()
+    if dev < 0:
+        raise RomError(f"{name} must be a contiguous CUDA tensor")
+    return dev
+
+
+def _ws(t, dev):
+    """Address and bytes of a workspace (or None)."""
+    if t is None:
+        return None, 0
+    if t.get_device() != dev or not t.is_contiguous():
+        raise RomError(f"ws must be a contiguous tensor on cuda:{dev}")
+    return t.data_ptr(), t.numel() * t.element_size()
+
+
+def _call(fn, dev, stream, *args):
+    """Calls a library function with the stream as its last argument, on device
+    ``dev`` and its current stream unless one is given."""
     if stream is None:
-        # the handle alone: a Stream object costs 1.2 us of a 10 us call
-        handle = torch._C._cuda_getCurrentRawStream(index)
-    elif stream.device.index == index:
+        # the handle alone: a Stream object costs 1.2 us of a 9 us call
+        handle = torch._C._cuda_getCurrentRawStream(dev)
+    elif stream.device.index == dev:
         handle = stream.cuda_stream
     else:
-        raise RomError(f"{fn}: the stream is not one of cuda:{index}")
-    lib = _lib or load_library()
-    if torch.cuda.current_device() == index:
-        code = getattr(lib, fn)(*args, handle)
+        raise RomError(f"{fn}: the stream is not one of cuda:{dev}")
+    f = getattr(_lib or load_library(), fn)
+    if torch.cuda.current_device() == dev:
+        code = f(*args, handle)
     else:
-        with torch.cuda.device(index):
-            code = getattr(lib, fn)(*args, handle)
+        with torch.cuda.device(dev):
+            code = f(*args, handle)
     if code != ROM_OK:
         _check(code, fn)
 
@@ -277,16 +286,16 @@ def rom_add_rmsnorm(x, residual, weight, eps, res_out, y, y8=None, y_scale=None,
     T, D = x.shape
     rt = residual.dtype if residual is not None else (res_out.dtype if res_out is not None else _F32)
     code = _dtype_code(x)
-    _call("rom_add_rmsnorm", stream, (x, residual, weight, res_out, y, y8, y_scale, rstd),
-          _t(x, "x", x.dtype, T, D), code,
-          None if residual is None else _t(residual, "residual", rt, T, D),
+    dev = _device(x, "x")
+    _call("rom_add_rmsnorm", dev, stream, _t(x, "x", x.dtype, (T, D), dev), code,
+          None if residual is None else _t(residual, "residual", rt, (T, D), dev),
           ROM_BF16 if rt is _BF16 else ROM_F32 if rt is _F32 else -1, T, D,
-          _t(weight, "weight", _F32, D), eps,
-          None if res_out is None else _t(res_out, "res_out", rt, T, D),
-          None if y is None else _t(y, "y", x.dtype, T, D),
-          None if y8 is None else _t(y8, "y8", _E4M3, T, D),
-          None if y_scale is None else _t(y_scale, "y_scale", _F32, T),
-          None if rstd is None else _t(rstd, "rstd", _F32, T))
+          _t(weight, "weight", _F32, (D,), dev), eps,
+          None if res_out is None else _t(res_out, "res_out", rt, (T, D), dev),
+          None if y is None else _t(y, "y", x.dtype, (T, D), dev),
+          None if y8 is None else _t(y8, "y8", _E4M3, (T, D), dev),
+          None if y_scale is None else _t(y_scale, "y_scale", _F32, (T,), dev),
+          None if rstd is None else _t(rstd, "rstd", _F32, (T,), dev))
 
 
 def rom_add_rmsnorm_bwd_workspace_size(T: int, D: int) -> int:
@@ -301,27 +310,24 @@ def rom_add_rmsnorm_bwd(dy, dres_out, res_out, weight, rstd, dx, dres, dw, ws, s
     T, D = dy.shape
     rt = res_out.dtype
     code = _dtype_code(dy)
-    if ws is not None and not (ws.is_cuda and ws.is_contiguous()):
-        raise RomError("ws must be a contiguous CUDA tensor")
-    _call("rom_add_rmsnorm_bwd", stream, (dy, dres_out, res_out, weight, rstd, dx, dres, dw, ws),
-          _t(dy, "dy", dy.dtype, T, D), code,
-          None if dres_out is None else _t(dres_out, "dres_out", rt, T, D),
-          _t(res_out, "res_out", rt, T, D),
+    dev = _device(dy, "dy")
+    _call("rom_add_rmsnorm_bwd", dev, stream, _t(dy, "dy", dy.dtype, (T, D), dev), code,
+          None if dres_out is None else _t(dres_out, "dres_out", rt, (T, D), dev),
+          _t(res_out, "res_out", rt, (T, D), dev),
           ROM_BF16 if rt is _BF16 else ROM_F32 if rt is _F32 else -1, T, D,
-          _t(weight, "weight", _F32, D), _t(rstd, "rstd", _F32, T),
-          None if dx is None else _t(dx, "dx", dy.dtype, T, D),
-          None if dres is None else _t(dres, "dres", rt, T, D),
-          None if dw is None else _t(dw, "dw", _F32, D),
-          None if ws is None else ws.data_ptr(),
-          0 if ws is None else ws.numel() * ws.element_size())
+          _t(weight, "weight", _F32, (D,), dev), _t(rstd, "rstd", _F32, (T,), dev),
+          None if dx is None else _t(dx, "dx", dy.dtype, (T, D), dev),
+          None if dres is None else _t(dres, "dres", rt, (T, D), dev),
+          None if dw is None else _t(dw, "dw", _F32, (D,), dev), *_ws(ws, dev))
 
 
 def rom_quant_rows(x, q, scale, stream=None):
     """The rows of x [rows, K] as e4m3 codes ``q`` and a float32 scale each."""
     rows, K = x.shape
     code = _dtype_code(x)
-    _call("rom_quant_rows", stream, (x, q, scale), _t(x, "x", x.dtype, rows, K), code, rows, K,
-          _t(q, "q", _E4M3, rows, K), _t(scale, "scale", _F32, rows))
+    dev = _device(x, "x")
+    _call("rom_quant_rows", dev, stream, _t(x, "x", x.dtype, (rows, K), dev), code, rows, K,
+          _t(q, "q", _E4M3, (rows, K), dev), _t(scale, "scale", _F32, (rows,), dev))
 
 
 def rom_dispatch_q8(x8, x_scale, E, k, topk_idx, ws, offsets, sorted_slot, slot_pos, x8_sorted,
@@ -329,15 +335,15 @@ def rom_dispatch_q8(x8, x_scale, E, k, topk_idx, ws, offsets, sorted_slot, slot_
     T, D = x8.shape
     R = T * k
     n = max(R, 1)
-    if ws is not None and not (ws.is_cuda and ws.is_contiguous()):
-        raise RomError("ws must be a contiguous CUDA tensor")
-    _call("rom_dispatch_q8", stream,
-          (x8, x_scale, topk_idx, ws, offsets, sorted_slot, slot_pos, x8_sorted, scale_sorted),
-          _t(x8, "x8", _E4M3, T, D), _t(x_scale, "x_scale", _F32, T), T, D, E, k,
-          _t(topk_idx, "topk_idx", _I32, T, k), None if ws is None else ws.data_ptr(),
-          0 if ws is None else ws.numel() * ws.element_size(), _t(offsets, "offsets", _I32, E + 1),
-          _t(sorted_slot, "sorted_slot", _I32, n), _t(slot_pos, "slot_pos", _I32, n),
-          _t(x8_sorted, "x8_sorted", _E4M3, n, D), _t(scale_sorted, "scale_sorted", _F32, n))
+    dev = _device(x8, "x8")
+    _call("rom_dispatch_q8", dev, stream, _t(x8, "x8", _E4M3, (T, D), dev),
+          _t(x_scale, "x_scale", _F32, (T,), dev), T, D, E, k,
+          _t(topk_idx, "topk_idx", _I32, (T, k), dev), *_ws(ws, dev),
+          _t(offsets, "offsets", _I32, (E + 1,), dev),
+          _t(sorted_slot, "sorted_slot", _I32, (n,), dev),
+          _t(slot_pos, "slot_pos", _I32, (n,), dev),
+          _t(x8_sorted, "x8_sorted", _E4M3, (n, D), dev),
+          _t(scale_sorted, "scale_sorted", _F32, (n,), dev))
 
 
 def rom_expert_proj_q8(proj, a_sorted, a_scale, w0, w0_scale, w1, w1_scale, k, offsets,
@@ -346,31 +352,30 @@ def rom_expert_proj_q8(proj, a_sorted, a_scale, w0, w0_scale, w1, w1_scale, k, o
     scales [R] and [E, N]. ``out`` as there, in bf16 or (slot rows) float32."""
     R, K = a_sorted.shape
     E, N, _ = w0.shape
+    dev = _device(a_sorted, "a_sorted")
     gate = proj == ROM_PROJ_CONV_GATE or proj == ROM_PROJ_CONV_GATE_SLOTS
     if gate and (w1 is None or w1_scale is None):
         raise RomError("the Conv+Gate projections need w1 and w1_scale")
     if k < 1 or R % k:
         raise RomError(f"{R} rows are no multiple of k = {k}")
     if k == 1 and (proj == ROM_PROJ_OUT or proj == ROM_PROJ_INPROJ or proj == ROM_PROJ_CONV_GATE):
-        po = _t(out, "out", _BF16, R, N)
+        po = _t(out, "out", _BF16, (R, N), dev)
     else:
         shape = (2, R, N) if gate else (R, N)
-        po = _t(out, "out", _F32, *shape)
-    dense = offsets is None
+        po = _t(out, "out", _F32, shape, dev)
     if sorted_slot is not None and sorted_slot.shape[0] < R:
         raise RomError(f"sorted_slot must hold {R} slots")
     if topk_w is not None and topk_w.numel() != R:
         raise RomError(f"topk_w must hold {R} weights")
-    _call("rom_expert_proj_q8", stream,
-          (a_sorted, a_scale, w0, w0_scale, w1, w1_scale, offsets, sorted_slot, topk_w, out),
-          proj, _t(a_sorted, "a_sorted", _E4M3, R, K), _t(a_scale, "a_scale", _F32, R), R, K,
-          _t(w0, "w0", _E4M3, E, N, K), _t(w0_scale, "w0_scale", _F32, E, N),
-          _t(w1, "w1", _E4M3, E, N, K) if gate else None,
-          _t(w1_scale, "w1_scale", _F32, E, N) if gate else None, N, E, k,
-          None if dense else _t(offsets, "offsets", _I32, E + 1),
+    _call("rom_expert_proj_q8", dev, stream, proj, _t(a_sorted, "a_sorted", _E4M3, (R, K), dev),
+          _t(a_scale, "a_scale", _F32, (R,), dev), R, K, _t(w0, "w0", _E4M3, (E, N, K), dev),
+          _t(w0_scale, "w0_scale", _F32, (E, N), dev),
+          _t(w1, "w1", _E4M3, (E, N, K), dev) if gate else None,
+          _t(w1_scale, "w1_scale", _F32, (E, N), dev) if gate else None, N, E, k,
+          None if offsets is None else _t(offsets, "offsets", _I32, (E + 1,), dev),
           None if sorted_slot is None else _t(sorted_slot, "sorted_slot", _I32,
-                                              sorted_slot.shape[0]),
-          None if topk_w is None else _t(topk_w, "topk_w", _F32, *topk_w.shape), po)
+                                              (sorted_slot.shape[0],), dev),
+          None if topk_w is None else _t(topk_w, "topk_w", _F32, topk_w.shape, dev), po)
 
 
 def rom_quant_expert_weights_w4(w, group, q, s, stream=None):
@@ -382,9 +387,10 @@ def rom_quant_expert_weights_w4(w, group, q, s, stream=None):
         raise RomError(f"group must be 32, 64 or 128, got {group}")
     nt, kb = -(-N // 16), -(-K // 128)
     code = _dtype_code(w)
-    _call("rom_quant_expert_weights_w4", stream, (w, q, s), code, _t(w, "w", w.dtype, E, N, K), E,
-          N, K, group, _t(q, "q", torch.uint8, E, nt, kb, 2, 8, 4, 16),
-          _t(s, "s", _BF16, E, nt, kb, 16, 128 // group))
+    dev = _device(w, "w")
+    _call("rom_quant_expert_weights_w4", dev, stream, code, _t(w, "w", w.dtype, (E, N, K), dev), E,
+          N, K, group, _t(q, "q", torch.uint8, (E, nt, kb, 2, 8, 4, 16), dev),
+          _t(s, "s", _BF16, (E, nt, kb, 16, 128 // group), dev))
 
 
 def rom_expert_proj_w4(proj, x, q0, s0, q1, s1, N, k, topk_idx, topk_w, out, stream=None):
@@ -394,6 +400,7 @@ def rom_expert_proj_w4(proj, x, q0, s0, q1, s1, N, k, topk_idx, topk_w, out, str
     [T*k, N]; ROM_PROJ_CONV_GATE_SLOTS (with q1, s1): float32 [2, T*k, N]."""
     T, K = x.shape
     E, nt, kb = q0.shape[:3]
+    dev = _device(x, "x")
     if nt != -(-N // 16) or kb != -(-K // 128):
         raise RomError(f"q0 {list(q0.shape)} does not hold {N} x {K} weights")
     groups = s0.shape[-1]
@@ -403,18 +410,18 @@ def rom_expert_proj_w4(proj, x, q0, s0, q1, s1, N, k, topk_idx, topk_w, out, str
     if gate != (q1 is not None) or gate != (s1 is not None):
         raise RomError("q1 and s1 go with ROM_PROJ_CONV_GATE_SLOTS, and only with it")
     if gate:
-        po = _t(out, "out", _F32, 2, T * k, N)
+        po = _t(out, "out", _F32, (2, T * k, N), dev)
     elif k == 1 and proj != ROM_PROJ_SLOTS:
-        po = _t(out, "out", _BF16, T, N)
+        po = _t(out, "out", _BF16, (T, N), dev)
     else:
-        po = _t(out, "out", _F32, T * k, N)
+        po = _t(out, "out", _F32, (T * k, N), dev)
     qs, ss = (E, nt, kb, 2, 8, 4, 16), (E, nt, kb, 16, groups)
-    _call("rom_expert_proj_w4", stream, (x, q0, s0, q1, s1, topk_idx, topk_w, out), proj,
-          _t(x, "x", _BF16, T, K), T, K, _t(q0, "q0", torch.uint8, *qs), _t(s0, "s0", _BF16, *ss),
-          _t(q1, "q1", torch.uint8, *qs) if gate else None,
-          _t(s1, "s1", _BF16, *ss) if gate else None, N, E, k, 128 // groups,
-          _t(topk_idx, "topk_idx", _I32, T, k),
-          None if topk_w is None else _t(topk_w, "topk_w", _F32, T, k), po)
+    _call("rom_expert_proj_w4", dev, stream, proj, _t(x, "x", _BF16, (T, K), dev), T, K,
+          _t(q0, "q0", torch.uint8, qs, dev), _t(s0, "s0", _BF16, ss, dev),
+          _t(q1, "q1", torch.uint8, qs, dev) if gate else None,
+          _t(s1, "s1", _BF16, ss, dev) if gate else None, N, E, k, 128 // groups,
+          _t(topk_idx, "topk_idx", _I32, (T, k), dev),
+          None if topk_w is None else _t(topk_w, "topk_w", _F32, (T, k), dev), po)
 
 
 # ------------------------------------------------------------------ block helpers
@@ -658,8 +665,11 @@ def inproj_forward(x, w_r, w, k=1, renorm=False, bias=None, bufs=None, out=None,
 
 def _inproj_forward_w4(x, w_r, w, k, renorm, bias, bufs, out, slots, stream):
     T, Dm = x.shape
-    _t(x, "x", _BF16, T, w.K)
-    _t(w_r, "w_r", _F32, Dm, w.E)
+    dev = _device(x, "x")
+    _t(x, "x", _BF16, (T, w.K), dev)
+    _t(w_r, "w_r", _F32, (Dm, w.E), dev)
+    if bias is not None:
+        _t(bias, "bias", _F32, (w.E,), dev)
     with _scope(x, stream):
         if bufs is None:
             bufs = RoutingBuffers(T, Dm, w.E, k, x.dtype, x.device)
@@ -844,10 +854,11 @@ def block_forward_q8(x, w_r, bias, w_conv, w_gate, w_out, k, renorm=False, x8=No
     ``.out``)."""
     T, Dm = x.shape
     E, De = w_conv.E, w_conv.N
-    _t(x, "x", _BF16, T, w_conv.K)
-    _t(w_r, "w_r", _F32, Dm, E)
+    dev = _device(x, "x")
+    _t(x, "x", _BF16, (T, w_conv.K), dev)
+    _t(w_r, "w_r", _F32, (Dm, E), dev)
     if bias is not None:
-        _t(bias, "bias", _F32, E)
+        _t(bias, "bias", _F32, (E,), dev)
     if (x8 is None) != (x_scale is None):
         raise RomError("x8 and x_scale come together")
     if w_gate.q.shape != w_conv.q.shape or w_out.q.shape != (E, Dm, De):
@@ -899,10 +910,11 @@ def block_forward_w4(x, w_r, bias, w_conv, w_gate, w_out, k, renorm=False, bufs=
     dispatch. Any T, 64 tokens at a time; meant for few. x [T, Dm] bf16.
     Returns the W4BlockBuffers (O in ``.out``)."""
     T, Dm = x.shape
-    _t(x, "x", _BF16, T, w_conv.K)
-    _t(w_r, "w_r", _F32, Dm, w_conv.E)
+    dev = _device(x, "x")
+    _t(x, "x", _BF16, (T, w_conv.K), dev)
+    _t(w_r, "w_r", _F32, (Dm, w_conv.E), dev)
     if bias is not None:
-        _t(bias, "bias", _F32, w_conv.E)
+        _t(bias, "bias", _F32, (w_conv.E,), dev)
     if w_out.K != w_conv.N or w_out.N != Dm or w_gate.q.shape != w_conv.q.shape:
         raise RomError("the 4-bit weights' sizes do not fit together")
     De = w_conv.N
