@@ -61,6 +61,11 @@ constexpr int kThreads = 192;
 // Out / in-projection calls with at most this many routed rows use the
 // swap-AB kernel (weights on the MMA's M side).
 constexpr int64_t kSwapMaxRows = 1024;
+// In 8 bits, calls with at most this many routed rows per expert on average, as
+// measured (us, swap-AB against the pair kernel, K 2048, N 2048 unless stated):
+// 8 rows per expert of 8, K 4096: 12.7 / 18.4; 32 of 64, N 1024: 36 / 66; 64 of 8:
+// 14.9 / 15.1; 91 of 33, K and N 1024: 22.0 / 19.5; 128 of 8: 19.8 / 15.7.
+constexpr int64_t kSwapMaxRowsPerExpertQ8 = 64;
 
 struct Params {
   const int32_t* offsets;
@@ -125,8 +130,8 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
 }
 
 // Epilogue of one accumulator tile for one warp: thread i reads TMEM lane
-// t_row.lane + i, i.e. sorted row `prow` (stored only when `valid`), output
-// columns n0 .. n0 + w - 1 (w = 128 for the gate modes, whose z columns
+// t_row.lane + i, i.e. sorted row `prow` (stored only when `valid`), the
+// 32-column chunks c0 .. c1 - 1 of output columns n0 .. n0 + w - 1 (w = 128 for the gate modes, whose z columns
 // follow the w u columns in TMEM, 256 otherwise; half of that for the half
 // tiles of a last wave). The
 // float32 outputs (per-slot partials) go row by row through the warp's
@@ -134,7 +139,8 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
 // are stored directly in 16-byte pieces, which measured faster for them.
 template <int MODE, bool kQ8>
 __device__ __forceinline__ void epilogue_rows(const Params& p, uint32_t t_row, bool valid,
-                                              int64_t prow, int e, int n0, int w, float* stg) {
+                                              int64_t prow, int e, int n0, int w, int c0, int c1,
+                                              float* stg) {
   // this row's scale and the tile's columns' (8-bit products)
   const float sa = kQ8 && valid ? p.a_scale[prow] : 0.f;
   const float* sw0 = kQ8 ? p.w0_scale + static_cast<int64_t>(e) * p.N + n0 : nullptr;
@@ -142,7 +148,7 @@ __device__ __forceinline__ void epilogue_rows(const Params& p, uint32_t t_row, b
   if (MODE == kEpiGateH) {
     __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out);
 #pragma unroll 1
-    for (int c = 0; c < w / 32; ++c) {
+    for (int c = c0; c < c1; ++c) {
       uint32_t u[32], z[32];
       tmem_ld32(t_row + c * 32, u);
       tmem_ld32(t_row + w + c * 32, z);
@@ -170,7 +176,7 @@ __device__ __forceinline__ void epilogue_rows(const Params& p, uint32_t t_row, b
     float* out = static_cast<float*>(p.out);
     const int64_t slot = valid ? slot_of(p, prow) : 0;
 #pragma unroll 1
-    for (int c = 0; c < w / 32; ++c) {
+    for (int c = c0; c < c1; ++c) {
       uint32_t u[32], z[32];
       tmem_ld32(t_row + c * 32, u);
       tmem_ld32(t_row + w + c * 32, z);
@@ -190,7 +196,7 @@ __device__ __forceinline__ void epilogue_rows(const Params& p, uint32_t t_row, b
     // no routing weights passed: r = 1
     const float r = valid ? (p.topk_w ? p.topk_w[slot] : 1.f) : 0.f;
 #pragma unroll 1
-    for (int c = 0; c < w / 32; ++c) {
+    for (int c = c0; c < c1; ++c) {
       if (n0 + c * 32 >= p.N) break;  // partial last tile (N % 256 == 128)
       uint32_t a[32];
       tmem_ld32(t_row + c * 32, a);
@@ -234,19 +240,25 @@ __device__ __forceinline__ void epilogue_rows(const Params& p, uint32_t t_row, b
 //             bytes; both producers' TMA loads complete on it.
 //   empty[s]  one per CTA: the MMA commit arrives on both (multicast).
 //   tfull[a]  one per CTA: the commit after a tile's last MMA, multicast.
-//   tempty[a] lives in CTA 0: the 4 epilogue warps of each CTA arrive
+//   tempty[a] lives in CTA 0: the epilogue warps of each CTA arrive
 //             (CTA 1's through the cluster window).
 // A CTA never exits while the other may still touch its shared memory or
 // TMEM: both end at a cluster barrier that every path reaches after bounded
 // waits.
 constexpr int PM = 256;                      // rows per pair tile
-// Ring depth: 7 stages for the bf16-output modes, 6 (plus the epilogue
+// Ring depth: 7 stages for the bf16-output modes, 6 or 5 (plus the epilogue
 // warps' staging tiles) for the float32-output modes.
 constexpr int P_MAX_STAGES = 7;
-template <int MODE>
+// Epilogue warps: 4, or 8 (two per 32 rows, half of the columns each, one stage
+// less for their staging tiles) for the float32 outputs of 8-bit products, whose
+// tiles' MMAs take half of bf16's time. For the bf16 outputs 8 measured no
+// different (Conv+Gate of 16384 tokens 227 us against 222).
+template <int MODE, bool kQ8>
 struct PairGeo {
   static constexpr bool kStaged = (MODE == kEpiGateSlots || MODE == kEpiScaleSlots);
-  static constexpr int kStages = kStaged ? 6 : 7;
+  static constexpr int kEpiWarps = kStaged && kQ8 ? 8 : 4;
+  static constexpr int kStages = !kStaged ? 7 : kQ8 ? 5 : 6;
+  static constexpr int kThreads = 64 + 32 * kEpiWarps;
 };
 constexpr int P_A_BYTES = BM * BK * 2;       // 16 KB: this CTA's 128 rows
 constexpr int P_B_BYTES = 128 * BK * 2;      // 16 KB: this CTA's half of B
@@ -267,14 +279,15 @@ struct PairCtl {
 
 constexpr size_t kPairCtlBytes = (sizeof(PairCtl) + 15) / 16 * 16;
 // ring, control block, the 4 epilogue warps' staging tiles, alignment slack
-template <int MODE>
+template <int MODE, bool kQ8>
 constexpr size_t pair_smem_bytes() {
-  return PairGeo<MODE>::kStages * P_STAGE_BYTES + kPairCtlBytes +
-         (PairGeo<MODE>::kStaged ? 4 * kStageFloats * sizeof(float) : 0) + 1024;
+  using Geo = PairGeo<MODE, kQ8>;
+  return Geo::kStages * P_STAGE_BYTES + kPairCtlBytes +
+         (Geo::kStaged ? Geo::kEpiWarps * kStageFloats * sizeof(float) : 0) + 1024;
 }
 
 template <int MODE, bool kQ8>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(PairGeo<MODE, kQ8>::kThreads, 1)
     tc_pair_gemm_kernel(const __grid_constant__ CUtensorMap tmA,
                         const __grid_constant__ CUtensorMap tmB0,
                         const __grid_constant__ CUtensorMap tmB1,
@@ -282,7 +295,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                         const __grid_constant__ CUtensorMap tmB1h, const Params p) {
   constexpr bool kGate = (MODE == kEpiGateH || MODE == kEpiGateSlots);
   constexpr int kTileN = kGate ? 128 : 256;  // output columns per tile
-  constexpr int P_STAGES = PairGeo<MODE>::kStages;
+  constexpr int P_STAGES = PairGeo<MODE, kQ8>::kStages;
+  constexpr int kEpiWarps = PairGeo<MODE, kQ8>::kEpiWarps;
   extern __shared__ uint8_t smem_raw[];
   // Same 1024-byte aligned offset in both CTAs (same kernel, same static
   // layout), as the pair MMA reads the peer's operands at the leader's offsets.
@@ -295,7 +309,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int pair = static_cast<int>(blockIdx.x >> 1);
   const int npairs = static_cast<int>(gridDim.x >> 1);
 
-  for (int i = threadIdx.x; i <= E; i += kThreads) ctl.off[i] = offset_of(p, i);
+  for (int i = threadIdx.x; i <= E; i += PairGeo<MODE, kQ8>::kThreads)
+    ctl.off[i] = offset_of(p, i);
   __syncthreads();
   if (threadIdx.x == 0) {
     int run = 0;
@@ -312,7 +327,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int a = 0; a < 2; ++a) {
       mbar_init(&ctl.tfull[a], 1);
-      mbar_init(&ctl.tempty[a], 8);
+      mbar_init(&ctl.tempty[a], 2 * kEpiWarps);
     }
     mbar_init(&ctl.drain, 1);
     ctl.abort = 0;
@@ -475,8 +490,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_wait(&ctl.drain, 0, &never, p.status);
     }
   } else {
-    // -------------------------------------------------- epilogue (warps 2..5)
-    const int q = warp & 3;
+    // -------------------------------------------------- epilogue (warps 2 ..)
+    const int q = warp & 3, part = (warp - 2) >> 2;
+    constexpr int kParts = kEpiWarps / 4;
     const uint32_t tempty0 = mapa_shared(smem_u32(&ctl.tempty[0]), 0);
     float* stg = reinterpret_cast<float*>(smem + P_STAGES * P_STAGE_BYTES + kPairCtlBytes) +
                  (warp - 2) * kStageFloats;
@@ -495,7 +511,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           tmem_base + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(acc * UMMA_N);
       const int w = half < 0 ? kTileN : kTileN / 2;
       epilogue_rows<MODE, kQ8>(p, t_row, valid, prow, e,
-                               n_blk * kTileN + (half < 0 ? 0 : half * w), w, stg);
+                               n_blk * kTileN + (half < 0 ? 0 : half * w), w,
+                               part * (w / 32) / kParts, (part + 1) * (w / 32) / kParts, stg);
       tc_fence_before();
       __syncwarp();
       if (lane == 0) {
@@ -850,7 +867,7 @@ cudaError_t launch_pair_mode(const CUtensorMap& a, const CUtensorMap& b0, const 
                              const CUtensorMap& b0h, const CUtensorMap& b1h, const Params& p,
                              int64_t max_tiles, cudaStream_t stream) {
   auto kern = tc_pair_gemm_kernel<MODE, kQ8>;
-  constexpr size_t kPairSmemBytes = pair_smem_bytes<MODE>();
+  constexpr size_t kPairSmemBytes = pair_smem_bytes<MODE, kQ8>();
   cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          static_cast<int>(kPairSmemBytes));
   if (err != cudaSuccess) return err;
@@ -860,7 +877,7 @@ cudaError_t launch_pair_mode(const CUtensorMap& a, const CUtensorMap& b0, const 
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.blockDim = dim3(kThreads, 1, 1);
+  cfg.blockDim = dim3(PairGeo<MODE, kQ8>::kThreads, 1, 1);
   cfg.dynamicSmemBytes = kPairSmemBytes;
   cfg.stream = stream;
   cfg.attrs = attr;
@@ -894,7 +911,7 @@ cudaError_t launch_grouped(int mode, const void* a_sorted, const float* a_scale,
   const bool gate = (mode == kEpiGateH || mode == kEpiGateSlots);
   const int tile_n = gate ? 128 : 256;
   // Few tokens (decode): the swap-AB kernel streams every weight tile once.
-  if (!gate && R <= kSwapMaxRows && N % SW_BM == 0 && K % kAlign == 0 && E <= kMaxExperts) {
+  if (!gate && R <= (kQ8 ? kSwapMaxRowsPerExpertQ8 * E : kSwapMaxRows) && N % SW_BM == 0 && K % kAlign == 0 && E <= kMaxExperts) {
     if (R == 0) return cudaSuccess;
     CUtensorMap tw, tx;
     if (!make_map<kQ8>(&tw, w0, K, N, E, SW_BM)) return cudaErrorInvalidValue;
