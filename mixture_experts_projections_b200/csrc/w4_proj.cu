@@ -51,6 +51,11 @@ constexpr int kW4MaxTokens = 64;
 constexpr int kW4MaxSlots = kW4MaxTokens * kMaxTopK;
 constexpr int kW4MaxStages = 6;
 constexpr int kW4MostSmem = 110 * 1024;   // of each of two CTAs on an SM
+constexpr int kW4ThirdSmem = 73 * 1024;   // of each of three
+// CTAs of `warps` consumer warps that an SM holds: their registers set it.
+__host__ __device__ constexpr int w4_resident(int nb, int warps) {
+  return nb == 1 && warps <= 7 ? 3 : 2;
+}
 
 struct W4Params {
   const __nv_bfloat16* x;
@@ -431,7 +436,8 @@ cudaError_t launch_w4(W4Params p, const W4Maps& maps, int warps, int mats, cudaS
   }
   const int row_blks = (p.nt + warps - 1) / warps;
   const int stage = w4_stage_bytes<NB>(warps);
-  const int budget = kW4MostSmem - static_cast<int>(sizeof(W4Ctl));
+  const int budget = (w4_resident(NB, warps) == 3 ? kW4ThirdSmem : kW4MostSmem) -
+                     static_cast<int>(sizeof(W4Ctl));
   p.stages = std::min(kW4MaxStages, budget / stage);
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -562,23 +568,32 @@ cudaError_t launch_w4_proj(const void* x, int T, int K, const void* q0, const vo
   p.status = status;
   p.max_active = std::min(E, T * k);
   const int mats = q1 ? 2 : 1;
+  // Token blocks of 8 held at a time: enough for an expert with two standard
+  // deviations more tokens than an even routing gives it (one with more is
+  // passed over again, its weights then coming from L2): fewer blocks leave room
+  // for more CTAs. 19 tokens, top-2 of 16 experts: 14.9 us with 1, 18.1 with 3; 32
+  // tokens, top-1 of 4: 29.0 with 2, 43 with 1.
+  const double even = static_cast<double>(T) * k / E;
+  const double most = std::min(static_cast<double>(T), even + 2.0 * std::sqrt(even));
+  const int nb = most <= 8.0 ? 1 : most <= 16.0 ? 2 : 3;
   // Shape of the work: CTAs of `warps` 16-row tiles, `splits` of them (a
   // cluster) sharing the columns of one row block. The cost is an SM's: the
   // tiles that its CTAs' warps go through, ceil(CTAs / SMs) * warps / splits,
-  // slower where few warps are resident (two CTAs fit) and where a third round
-  // starts late, plus the cluster's hand-over of its sums (1.5 tiles of 4096
-  // columns per split). Measured, us, at 4 experts of 10240 x 4096: one token 10.9 (9
-  // warps, 2 splits; 12.6 with 4 and 1, 14.0 with 9 and 4), 4 tokens 14.2 (9 and
-  // 2; 15.0 with 5 and 1), 64 tokens 36.3 (9 and 1; 44 with 5, 47 with 8).
+  // slower where few warps are resident and where CTAs start late, plus the
+  // cluster's hand-over of its sums (1.5 tiles of 4096 columns per split).
+  // Measured, us, at 4 experts of 10240 x 4096: one token 10.9 (9 warps, 2
+  // splits; 12.6 with 4 and 1, 14.0 with 9 and 4), 4 tokens 14.2 (9 and 2; 15.0
+  // with 5 and 1), 64 tokens 36.3 (9 and 1; 44 with 5, 47 with 8).
   const double used = E * (1.0 - std::pow(1.0 - static_cast<double>(k) / E, T));
   const int sms = device_sm_count();
   int warps = kW4MaxWarps;
   double best = 1e30;
   for (int s = 1; s <= 8 && (s == 1 || p.kb / s >= 4); s *= 2) {
     for (int w = kW4MaxWarps; w >= kW4MinWarps; --w) {
-      const double rounds = std::ceil(std::ceil(((p.nt + w - 1) / w) * used * mats * s) / sms);
-      const double resident = std::min(rounds, 2.0) * w;
-      const double cost = rounds * w / s * (1.0 + 6.0 / resident) * (rounds > 2 ? 1.1 : 1.0) +
+      const double ctas = std::ceil(std::ceil(((p.nt + w - 1) / w) * used * mats * s) / sms);
+      const int room = w4_resident(nb, w);
+      const double resident = std::min(ctas, static_cast<double>(room)) * w;
+      const double cost = ctas * w / s * (1.0 + 6.0 / resident) * (ctas > room ? 1.1 : 1.0) +
                           (s > 1 ? 1.5 * s * 32.0 / p.kb : 0.0);
       if (cost < best * 0.999) {
         best = cost;
@@ -597,8 +612,8 @@ cudaError_t launch_w4_proj(const void* x, int T, int K, const void* q0, const vo
     maps.q[1] = maps.q[0];
     maps.s[1] = maps.s[0];
   }
-  if (T <= 8) return launch_w4_group<1>(p, maps, warps, mats, group, stream);
-  if (T <= 16) return launch_w4_group<2>(p, maps, warps, mats, group, stream);
+  if (nb == 1) return launch_w4_group<1>(p, maps, warps, mats, group, stream);
+  if (nb == 2) return launch_w4_group<2>(p, maps, warps, mats, group, stream);
   return launch_w4_group<3>(p, maps, warps, mats, group, stream);
 }
 
