@@ -377,3 +377,28 @@ def test_binding_refuses_wrong_tensors():
         rom.rom_quant_rows(x, torch.zeros(4, 64, dtype=torch.uint8, device="cuda"), torch.zeros(4, device="cuda"))
     with pytest.raises(rom.RomError, match="WORKSPACE"):
         rom.rom_add_rmsnorm_bwd(x, None, res, w, torch.ones(4, device="cuda"), y, None, w.clone(), None)
+
+
+@gpu
+def test_rows_past_two_to_the_31_elements():
+    """A batch of more than 2^31 elements: its last rows are those of a small
+    batch (a row's result does not depend on the others)."""
+    D = 8192
+    T = (1 << 31) // D + 3
+    x = torch.empty(T, D, dtype=BF16, device="cuda")
+    x.normal_(generator=torch.Generator(device="cuda").manual_seed(0))
+    w = torch.ones(D, device="cuda")
+    n = rom.add_rmsnorm(x, None, w, q8=True, residual_dtype=BF16)
+    m = rom.add_rmsnorm(x[-4:].contiguous(), None, w, q8=True, residual_dtype=BF16)
+    for a, b in ((n.y, m.y), (n.residual, m.residual), (n.y8.view(torch.uint8), m.y8.view(torch.uint8)),
+                 (n.y_scale, m.y_scale), (n.rstd, m.rstd)):
+        assert torch.equal(a[-4:], b)
+    q, s = rom.quant_rows(n.y)
+    q4, s4 = rom.quant_rows(m.y)
+    assert torch.equal(q[-4:].view(torch.uint8), q4.view(torch.uint8)) and torch.equal(s[-4:], s4)
+    del n.y8, q
+    dx = torch.empty_like(x)
+    rom.rom_add_rmsnorm_bwd(n.y, None, n.residual, w, n.rstd, dx, None, None, None)
+    dx4 = torch.empty_like(m.y)
+    rom.rom_add_rmsnorm_bwd(m.y, None, m.residual, w, m.rstd, dx4, None, None, None)
+    assert torch.equal(dx[-4:], dx4)

@@ -87,6 +87,8 @@ CASES = [
     # T, K, N, E, k, pin
     (1, 64, 128, 4, 1, None), (300, 128, 256, 8, 1, None), (77, 1008, 384, 5, 1, None),
     (64, 400, 128, 64, 8, None), (1500, 256, 128, 8, 1, None), (700, 272, 384, 33, 2, None),
+    # both sides of the 64 rows per expert at which the kernels change
+    (256, 144, 128, 4, 1, None), (257, 144, 128, 4, 1, None), (33, 96, 128, 2, 2, 1),
     (1300, 160, 256, 4, 1, 2), (2, 16, 128, 1, 1, None), (300, 2048, 640, 3, 2, None),
 ]
 

@@ -115,6 +115,8 @@ CASES = [
     (1, 64, 16, 1, 1, 128, None), (1, 4096, 130, 4, 1, 128, None), (5, 1000, 37, 4, 2, 32, None),
     (8, 128, 128, 8, 1, 64, None), (9, 2056, 300, 3, 3, 64, None), (16, 520, 1, 16, 2, 32, None),
     (17, 384, 260, 5, 1, 128, None), (64, 256, 144, 4, 1, 32, None), (64, 640, 50, 64, 8, 64, None),
+    # columns shared by a cluster, once over the tokens and (all 64 on one expert) several times
+    (3, 8192, 16, 1, 1, 64, None), (64, 4096, 130, 4, 1, 128, 2), (40, 2048, 20, 16, 2, 32, 3),
     (64, 768, 140, 4, 1, 128, 2), (33, 8, 8, 2, 2, 32, None), (40, 1160, 129, 2, 1, 128, 0),
 ]
 
@@ -341,3 +343,20 @@ def test_w4_binding_refuses_wrong_tensors():
             rom.rom_expert_proj_w4(**{**ok, **bad})
     with pytest.raises(rom.RomError, match="group must be"):
         rom.W4Weights.quantize(torch.zeros(1, 16, 64, device="cuda"), 16)
+
+
+@gpu
+def test_w4_calls_on_two_streams_at_once():
+    q, s = (t.cuda() for t in random_w4(4, 1000, 2048, 64, seed=0))
+    x = torch.randn(32, 2048, generator=torch.Generator().manual_seed(1)).to(BF16).cuda()
+    idx, r, _, _ = make_routing(32, 4, 2, 3)
+    idx, r = torch.from_numpy(idx).cuda(), torch.from_numpy(r).cuda()
+    outs = [torch.empty(64, 1000, device="cuda") for _ in range(9)]
+    args = (rom.ROM_PROJ_OUT, x, q, s, None, None, 1000, 2, idx, r)
+    rom.rom_expert_proj_w4(*args, outs[8])
+    torch.cuda.synchronize()
+    st = [torch.cuda.Stream() for _ in range(2)]
+    for i in range(8):
+        rom.rom_expert_proj_w4(*args, outs[i], stream=st[i % 2])
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, outs[8]) for o in outs[:8]) and rom.rom_get_status() == 0
