@@ -383,7 +383,9 @@ __global__ void __maxnreg__(96)
     const int rows = warps * 16 / p.splits;  // this rank's share of the rows
     const int row0 = rank * rows, n0 = row_blk * warps * 16 + row0;
     const int n_rows = *abort_flag ? 0 : min(rows, p.N - n0);
-    for (int j = warp; j < n_tok; j += warps + 1) {
+    // a warp per token, or several that share its rows
+    const int share = max(1, (warps + 1) / n_tok), turn = (warps + 1) / share;
+    for (int j = warp / share; j < n_tok; j += turn) {
       const float r = ctl.weight[p0 + j];
       const int slot = ctl.slot[p0 + j];
       const float* from = red + j * pitch + row0;
@@ -391,7 +393,7 @@ __global__ void __maxnreg__(96)
       float* o32 =
           static_cast<float*>(p.out) + (static_cast<int64_t>(mat) * nslots + slot) * p.N + n0;
 #pragma unroll 4
-      for (int i = lane; i < n_rows; i += 32) {
+      for (int i = warp % share * 32 + lane; i < n_rows; i += 32 * share) {
         float v;
         if (p.splits > 1) {
           const uint32_t at = smem_u32(from + i);
