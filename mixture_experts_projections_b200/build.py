@@ -4,8 +4,9 @@
 
 Compiles every csrc/*.cu with nvcc for sm_100a only, in parallel, and links
 them (with the static CUDA runtime) into mixture_experts_projections_b200/
-librom.so. Objects go to mixture_experts_projections_b200/_build/. Sources
-are rebuilt only when they, or a header under csrc/ or include/, changed.
+librom.so, and binding/fast_calls.cpp with g++ against the installed torch
+into _fast_calls.so. Objects go to mixture_experts_projections_b200/_build/.
+Sources are rebuilt only when they, or a header under csrc/ or include/, changed.
 """
 from __future__ import annotations
 
@@ -23,6 +24,8 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "librom.so")
+FAST_SRC = os.path.join(PKG, "binding", "fast_calls.cpp")
+FAST = os.path.join(PKG, "_fast_calls.so")
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 CFLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC",
@@ -64,12 +67,34 @@ def _compile(src: str, verbose: bool, force: bool) -> str:
     return obj
 
 
+def _build_fast_calls(force: bool) -> None:
+    """The binding's checked calls (a Python extension on torch's C++ API)."""
+    if (not force and os.path.exists(FAST)
+            and os.path.getmtime(FAST) >= max(os.path.getmtime(FAST_SRC), _deps_mtime(FAST_SRC))):
+        return
+    import sysconfig
+
+    import torch
+    from torch.utils.cpp_extension import include_paths, library_paths
+    cuda_inc = os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include")
+    inc = include_paths() + [cuda_inc, sysconfig.get_paths()["include"]]
+    cmd = (["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wno-unknown-pragmas",
+            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", FAST_SRC, "-o", FAST]
+           + [f"-isystem{p}" for p in inc]
+           + [f"-L{p}" for p in library_paths()] + ["-ltorch_python", "-ltorch_cpu", "-lc10_cuda", "-lc10"])
+    res = subprocess.run(cmd, capture_output=True, text=True)
+    if res.returncode != 0:
+        raise RuntimeError(f"g++ failed for {FAST_SRC}:\n{res.stdout}\n{res.stderr}")
+
+
 def build(verbose: bool = False, force: bool = False) -> str:
-    """Compile and link librom.so; returns its path."""
+    """Compile and link librom.so and the binding's extension; returns librom.so's path."""
     os.makedirs(BUILD, exist_ok=True)
     srcs = sorted(glob.glob(os.path.join(CSRC, "*.cu")))
-    with cf.ThreadPoolExecutor(max_workers=min(8, len(srcs))) as ex:
+    with cf.ThreadPoolExecutor(max_workers=min(8, len(srcs) + 1)) as ex:
+        fast = ex.submit(_build_fast_calls, force)
         objs = list(ex.map(lambda s: _compile(s, verbose, force), srcs))
+        fast.result()
     if (force or not os.path.exists(LIB)
             or os.path.getmtime(LIB) < max(os.path.getmtime(o) for o in objs)):
         cmd = [nvcc()] + ARCH + ["-shared", "-cudart", "static", "-o", LIB] + objs

@@ -74,6 +74,11 @@ SIGNATURES = {
 }
 
 _lib = None
+# binding/fast_calls.cpp, once the library is loaded (None where it is not built:
+# the calls below then check their tensors in Python, at 0.4 us each).
+_fast = None
+_FAST_CALLS = ("rom_add_rmsnorm", "rom_add_rmsnorm_bwd", "rom_quant_rows", "rom_expert_proj_q8",
+               "rom_expert_proj_w4")
 
 
 class RomError(RuntimeError):
@@ -93,7 +98,26 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
             fn.restype = res
             fn.argtypes = args
         _lib = lib
+        if path == LIB_PATH and os.path.exists(os.path.join(_HERE, "_fast_calls.so")):
+            _load_fast_calls(lib)
     return _lib
+
+
+def _load_fast_calls(lib):
+    global _fast
+    from . import _fast_calls
+    _fast_calls.bind(*(ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in _FAST_CALLS))
+    _fast = _fast_calls
+
+
+def _fast_done(code, fn):
+    """Whether a call of _fast was made (it returns None where its arguments are
+    not what it takes); raises its error."""
+    if code is None:
+        return False
+    if code != ROM_OK:
+        _check(code, fn)
+    return True
 
 
 def _check(code: int, what: str):
@@ -283,6 +307,10 @@ def rom_add_rmsnorm(x, residual, weight, eps, res_out, y, y8=None, y_scale=None,
     weight with rstd = 1 / sqrt(mean s^2 + eps), per row of [T, Dm]. Any of the
     outputs may be None; ``y8`` (e4m3) and ``y_scale`` come together. The
     residual stream's type is that of ``residual`` or ``res_out``."""
+    if stream is None and _fast is not None and _fast_done(
+            _fast.add_rmsnorm(x, residual, weight, eps, res_out, y, y8, y_scale, rstd),
+            "rom_add_rmsnorm"):
+        return
     T, D = x.shape
     rt = residual.dtype if residual is not None else (res_out.dtype if res_out is not None else _F32)
     code = _dtype_code(x)
@@ -307,6 +335,10 @@ def rom_add_rmsnorm_bwd(dy, dres_out, res_out, weight, rstd, dx, dres, dw, ws, s
     may be ``dres_out``) are the same values, dw float32 [Dm]; each may be
     None, and so may ``dres_out``. ``ws``: at least
     rom_add_rmsnorm_bwd_workspace_size(T, Dm) bytes, for dw."""
+    if stream is None and _fast is not None and _fast_done(
+            _fast.add_rmsnorm_bwd(dy, dres_out, res_out, weight, rstd, dx, dres, dw, ws),
+            "rom_add_rmsnorm_bwd"):
+        return
     T, D = dy.shape
     rt = res_out.dtype
     code = _dtype_code(dy)
@@ -323,6 +355,9 @@ def rom_add_rmsnorm_bwd(dy, dres_out, res_out, weight, rstd, dx, dres, dw, ws, s
 
 def rom_quant_rows(x, q, scale, stream=None):
     """The rows of x [rows, K] as e4m3 codes ``q`` and a float32 scale each."""
+    if stream is None and _fast is not None and _fast_done(_fast.quant_rows(x, q, scale),
+                                                           "rom_quant_rows"):
+        return
     rows, K = x.shape
     code = _dtype_code(x)
     dev = _device(x, "x")
@@ -350,6 +385,10 @@ def rom_expert_proj_q8(proj, a_sorted, a_scale, w0, w0_scale, w1, w1_scale, k, o
                        sorted_slot, topk_w, out, stream=None):
     """rom_expert_proj on e4m3 rows [R, K] and weights [E, N, K] with float32
     scales [R] and [E, N]. ``out`` as there, in bf16 or (slot rows) float32."""
+    if stream is None and _fast is not None and _fast_done(
+            _fast.expert_proj_q8(proj, a_sorted, a_scale, w0, w0_scale, w1, w1_scale, k, offsets,
+                                 sorted_slot, topk_w, out), "rom_expert_proj_q8"):
+        return
     R, K = a_sorted.shape
     E, N, _ = w0.shape
     dev = _device(a_sorted, "a_sorted")
@@ -398,6 +437,10 @@ def rom_expert_proj_w4(proj, x, q0, s0, q1, s1, N, k, topk_idx, topk_w, out, str
     token order without a dispatch. ROM_PROJ_OUT and ROM_PROJ_INPROJ: weighted,
     out bf16 [T, N] (k == 1) or float32 [T*k, N]; ROM_PROJ_SLOTS: float32
     [T*k, N]; ROM_PROJ_CONV_GATE_SLOTS (with q1, s1): float32 [2, T*k, N]."""
+    if stream is None and _fast is not None and _fast_done(
+            _fast.expert_proj_w4(proj, x, q0, s0, q1, s1, N, k, topk_idx, topk_w, out),
+            "rom_expert_proj_w4"):
+        return
     T, K = x.shape
     E, nt, kb = q0.shape[:3]
     dev = _device(x, "x")
