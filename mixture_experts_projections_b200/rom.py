@@ -763,6 +763,10 @@ class Q8Weights:
         q, scale = quant_rows(w.view(E * N, K), stream)
         return cls(q.view(E, N, K), scale.view(E, N))
 
+    def dequantize(self):
+        """The float32 values [E, N, K] that the codes stand for."""
+        return self.q.float() * self.scale.unsqueeze(-1)
+
 
 class W4Weights:
     """Expert weights [E, N, K] in 4 bits with a bf16 scale per ``group``
@@ -785,6 +789,17 @@ class W4Weights:
             s = torch.empty((E, nt, kb, 16, 128 // group), dtype=torch.bfloat16, device=w.device)
             rom_quant_expert_weights_w4(w, group, q, s, stream)
         return cls(q, s, N, K)
+
+    def dequantize(self):
+        """The float32 values [E, N, K] that the codes stand for (plain torch
+        operations: for checks and export, not for a hot path)."""
+        E, nt, kb = self.q.shape[:3]
+        v = torch.stack((self.q & 15, self.q >> 4), -1).float() - 8.0
+        # .., half, 8 rows, lane, word, then the three bits of a nibble's place
+        v = v.view(E, nt, kb, 2, 8, 4, 4, 2, 2, 2).permute(0, 1, 3, 4, 2, 6, 8, 5, 9, 7)
+        s = self.s.float().permute(0, 1, 3, 2, 4).reshape(E, nt * 16, kb, 128 // self.group, 1)
+        v = v.reshape(E, nt * 16, kb, 128 // self.group, self.group) * s
+        return v.reshape(E, nt * 16, kb * 128)[:, :self.N, :self.K].contiguous()
 
 
 # Tokens of one rom_expert_proj_w4 call.

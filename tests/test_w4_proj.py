@@ -221,6 +221,7 @@ def test_quantiser_gives_the_definitions_codes(E, N, K, group, dtype):
     q = q.reshape(E, N, -1)[..., :K].numpy()
     s = s.repeat_interleave(group, -1)[..., :K].numpy()
     assert np.array_equal(codes, q) and np.array_equal(scale, s)
+    assert np.array_equal(p.dequantize().cpu().numpy(), (val).astype(np.float32))
     # padding: codes 8, scales 0
     byte, shift = w4_position(-(-N // 16) * 16, -(-K // 128) * 128)
     allc = (p.q.cpu().numpy().reshape(E, -1)[:, byte] >> shift) & 15
