@@ -155,8 +155,9 @@ __device__ __forceinline__ void epilogue_rows(const Params& p, uint32_t t_row, b
       tmem_ld_wait();
       apply_scales<kQ8>(u, sa, sw0 + c * 32);
       apply_scales<kQ8>(z, sa, sw1 + c * 32);
-      if (valid) {
+      if (valid || kQ8) {
         uint4* dst = reinterpret_cast<uint4*>(out + prow * p.N + n0 + c * 32);
+        uint4 ws[4];
 #pragma unroll
         for (int v = 0; v < 4; ++v) {
           uint4 w;
@@ -168,8 +169,12 @@ __device__ __forceinline__ void epilogue_rows(const Params& p, uint32_t t_row, b
                           silu_gate(__uint_as_float(u[8 * v + 5]), __uint_as_float(z[8 * v + 5])));
           w.w = pack_bf16(silu_gate(__uint_as_float(u[8 * v + 6]), __uint_as_float(z[8 * v + 6])),
                           silu_gate(__uint_as_float(u[8 * v + 7]), __uint_as_float(z[8 * v + 7])));
-          dst[v] = w;
+          if (kQ8)
+            ws[v] = w;
+          else
+            dst[v] = w;
         }
+        if (kQ8) store_rows_bf16(reinterpret_cast<uint8_t*>(stg), ws, valid ? dst : nullptr);
       }
     }
   } else if (MODE == kEpiGateSlots) {
@@ -203,9 +208,10 @@ __device__ __forceinline__ void epilogue_rows(const Params& p, uint32_t t_row, b
       tmem_ld_wait();
       apply_scales<kQ8>(a, sa, sw0 + c * 32);
       if (MODE == kEpiScaleToken) {
-        if (valid) {
+        if (valid || kQ8) {
           __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out);
           uint4* dst = reinterpret_cast<uint4*>(out + (slot / p.k) * p.N + n0 + c * 32);
+          uint4 ws[4];
 #pragma unroll
           for (int v = 0; v < 4; ++v) {
             uint4 w;
@@ -213,8 +219,12 @@ __device__ __forceinline__ void epilogue_rows(const Params& p, uint32_t t_row, b
             w.y = pack_bf16(r * __uint_as_float(a[8 * v + 2]), r * __uint_as_float(a[8 * v + 3]));
             w.z = pack_bf16(r * __uint_as_float(a[8 * v + 4]), r * __uint_as_float(a[8 * v + 5]));
             w.w = pack_bf16(r * __uint_as_float(a[8 * v + 6]), r * __uint_as_float(a[8 * v + 7]));
-            dst[v] = w;
+            if (kQ8)
+              ws[v] = w;
+            else
+              dst[v] = w;
           }
+          if (kQ8) store_rows_bf16(reinterpret_cast<uint8_t*>(stg), ws, valid ? dst : nullptr);
         }
       } else {
         float f[32];
@@ -246,18 +256,19 @@ __device__ __forceinline__ void epilogue_rows(const Params& p, uint32_t t_row, b
 // TMEM: both end at a cluster barrier that every path reaches after bounded
 // waits.
 constexpr int PM = 256;                      // rows per pair tile
-// Ring depth: 7 stages for the bf16-output modes, 6 or 5 (plus the epilogue
-// warps' staging tiles) for the float32-output modes.
+// Ring depth: 7 stages for the bf16-output modes, 6 (plus the epilogue warps'
+// staging tiles) for the float32-output modes.
 constexpr int P_MAX_STAGES = 7;
-// Epilogue warps: 4, or 8 (two per 32 rows, half of the columns each, one stage
-// less for their staging tiles) for the float32 outputs of 8-bit products, whose
-// tiles' MMAs take half of bf16's time. For the bf16 outputs 8 measured no
-// different (Conv+Gate of 16384 tokens 227 us against 222).
+// 8-bit products, whose tiles' MMAs take half of bf16's time, have 8 epilogue
+// warps (two per 32 rows, half of the columns each) and stage their bf16 outputs
+// too; their staging tiles cost a stage.
 template <int MODE, bool kQ8>
 struct PairGeo {
-  static constexpr bool kStaged = (MODE == kEpiGateSlots || MODE == kEpiScaleSlots);
-  static constexpr int kEpiWarps = kStaged && kQ8 ? 8 : 4;
-  static constexpr int kStages = !kStaged ? 7 : kQ8 ? 5 : 6;
+  static constexpr bool kF32 = (MODE == kEpiGateSlots || MODE == kEpiScaleSlots);
+  static constexpr int kEpiWarps = kQ8 ? 8 : 4;
+  static constexpr int kStages = (kF32 ? 6 : 7) - (kQ8 ? 1 : 0);
+  static constexpr int kStageTile =  // bytes per epilogue warp
+      kF32 ? kStageFloats * 4 : kQ8 ? kStageBf16Bytes : 0;
   static constexpr int kThreads = 64 + 32 * kEpiWarps;
 };
 constexpr int P_A_BYTES = BM * BK * 2;       // 16 KB: this CTA's 128 rows
@@ -278,12 +289,11 @@ struct PairCtl {
 };
 
 constexpr size_t kPairCtlBytes = (sizeof(PairCtl) + 15) / 16 * 16;
-// ring, control block, the 4 epilogue warps' staging tiles, alignment slack
+// ring, control block, the epilogue warps' staging tiles, alignment slack
 template <int MODE, bool kQ8>
 constexpr size_t pair_smem_bytes() {
   using Geo = PairGeo<MODE, kQ8>;
-  return Geo::kStages * P_STAGE_BYTES + kPairCtlBytes +
-         (Geo::kStaged ? Geo::kEpiWarps * kStageFloats * sizeof(float) : 0) + 1024;
+  return Geo::kStages * P_STAGE_BYTES + kPairCtlBytes + Geo::kEpiWarps * Geo::kStageTile + 1024;
 }
 
 template <int MODE, bool kQ8>
@@ -494,8 +504,8 @@ __global__ void __launch_bounds__(PairGeo<MODE, kQ8>::kThreads, 1)
     const int q = warp & 3, part = (warp - 2) >> 2;
     constexpr int kParts = kEpiWarps / 4;
     const uint32_t tempty0 = mapa_shared(smem_u32(&ctl.tempty[0]), 0);
-    float* stg = reinterpret_cast<float*>(smem + P_STAGES * P_STAGE_BYTES + kPairCtlBytes) +
-                 (warp - 2) * kStageFloats;
+    float* stg = reinterpret_cast<float*>(smem + P_STAGES * P_STAGE_BYTES + kPairCtlBytes +
+                                          (warp - 2) * PairGeo<MODE, kQ8>::kStageTile);
     int acc = 0;
     uint32_t acc_phase = 0;
     int tile, half;

@@ -336,6 +336,27 @@ __device__ __forceinline__ void store_rows_f32(float* stg, const float (&v)[32],
   __syncwarp();
 }
 
+// The same for 32 columns of bf16, 16 bytes of `v` per 8 columns: eight rows of
+// 64 consecutive bytes per instruction. Rows 80 bytes apart in the staging tile.
+constexpr int kStageBf16Bytes = 32 * 80;  // per warp
+
+__device__ __forceinline__ void store_rows_bf16(uint8_t* stg, const uint4 (&v)[4], void* row) {
+  const int lane = threadIdx.x & 31;
+  uint4* s4 = reinterpret_cast<uint4*>(stg + lane * 80);
+#pragma unroll
+  for (int j = 0; j < 4; ++j) s4[j] = v[j];
+  __syncwarp();
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int r = 8 * i + (lane >> 2), c = lane & 3;
+    uint4* dst = reinterpret_cast<uint4*>(
+        __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(row), r));
+    const uint4 x = reinterpret_cast<const uint4*>(stg + r * 80)[c];
+    if (dst) dst[c] = x;
+  }
+  __syncwarp();
+}
+
 // ------------------------------------------------------------------ SM pairs
 // A cluster of two CTAs on neighbouring SMs runs one tcgen05.mma of
 // M = 256 (cta_group::2): CTA v of the pair holds rows 128v .. 128v+127 of A,
