@@ -28,11 +28,16 @@
 #include <algorithm>
 
 #include "rom_internal.cuh"
+#include "sm100_ptx.cuh"
 
 namespace rom {
 namespace {
 
 constexpr float kE4m3Max = 448.0f;
+// Rows that a CTA of the backward goes through at a time: 8 of a warp each, or 4
+// to 2 of up to 1024 to 2048 columns.
+constexpr int kNormBwdWarps = 8;
+constexpr int kNormBwdGroups = 4;
 constexpr float kAmaxFloor = 7.888609052210118e-31f;  // 2^-100
 
 // 8 elements as they are stored, and their values.
@@ -97,18 +102,22 @@ __device__ __forceinline__ float as_stored(float v, const __nv_bfloat16*) {
   return __bfloat162float(__float2bfloat16_rn(v));
 }
 
-// A row's threads: one warp (kWarp; blockDim = (32, rows)) or the whole CTA.
-// Sums and maxima over them come back in every thread; the order of the
-// additions is fixed. `red` holds one value per warp and is written once per
-// kernel (or between barriers of the caller).
-template <bool kWarp>
+// A row's threads: one warp (kWarp; blockDim = (32, rows)), the whole CTA, or
+// (kGroups) one of its blockDim.y groups with a named barrier each. Sums and
+// maxima over them come back in every thread; the order of the additions is
+// fixed. `red` holds one value per warp and is written once per kernel (or
+// between barriers of the caller).
+template <bool kWarp, bool kGroups = false>
 __device__ __forceinline__ float row_sum(float v, float* red) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
   if (kWarp) return v;
   const int warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
   if ((threadIdx.x & 31) == 0) red[warp] = v;
-  __syncthreads();
+  if (kGroups)
+    named_barrier_sync(1 + threadIdx.y, blockDim.x);
+  else
+    __syncthreads();
   float s = 0.f;
   for (int i = 0; i < nw; ++i) s += red[i];
   return s;
@@ -258,14 +267,25 @@ __global__ void __launch_bounds__(512)
 // registers for it (with its loads after the sum's barrier, and
 // none ahead, the kernel took 179 us for 32768 x 2560 bf16 where the bytes take
 // 128).
-template <typename XT, typename RT, int V>
-__global__ void __launch_bounds__(512)
+// Short rows leave room for several in a CTA, each with threads of its own
+// (blockDim.y of them; a warp each for up to 512 columns, kWarp): the CTA's sums of
+// dw are theirs, added in order. With one row per CTA the workspace's 512 rows
+// left SMs half empty: 11564 x 112 bf16 took 20 us (8 here), 20000 x 1024 57 (38).
+// One step per thread is held to 64 registers, for 1024 threads per SM: without
+// the bound 20000 x 1024 took 48 us and 32768 x 2560 178 (136).
+template <typename XT, typename RT, int V, bool kWarp, bool kGroups>
+__global__ void __launch_bounds__(512, V == 1 ? 2 : 1)
     add_rmsnorm_bwd_kernel(const XT* __restrict__ dy, const RT* dres_out,
                            const RT* __restrict__ s, int64_t T, int D,
                            const float* __restrict__ w, const float* __restrict__ rstd,
                            XT* __restrict__ dx, RT* dres, float* __restrict__ dw_part) {
   constexpr bool kAhead = V <= 2;
-  __shared__ float red[2][32];
+  constexpr bool kSeveral = kWarp || kGroups;
+  __shared__ float red[2][kGroups ? kNormBwdGroups : 1][32];
+  __shared__ float group_dw[kSeveral ? 4096 : 1];  // [blockDim.y][D]
+  const int step = kWarp ? 32 : blockDim.x;
+  const int64_t row0 = kSeveral ? int64_t(blockIdx.x) * blockDim.y + threadIdx.y : blockIdx.x;
+  const int64_t row_step = kSeveral ? int64_t(gridDim.x) * blockDim.y : gridDim.x;
   float dw[V][8];
 #pragma unroll
   for (int i = 0; i < V; ++i)
@@ -281,7 +301,7 @@ __global__ void __launch_bounds__(512)
       r = rstd[row];
 #pragma unroll
       for (int i = 0; i < (kAhead ? V : 0); ++i) {
-        const int c = (threadIdx.x + i * blockDim.x) * 8;
+        const int c = (threadIdx.x + i * step) * 8;
         if (c < D) {
           rg[i] = load_raw(dy + base + c);
           rs[i] = load_raw(s + base + c);
@@ -290,9 +310,9 @@ __global__ void __launch_bounds__(512)
       }
     }
   };
-  if (kAhead) fetch(blockIdx.x);
+  if (kAhead) fetch(row0);
   int buf = 0;
-  for (int64_t row = blockIdx.x; row < T; row += gridDim.x, buf ^= 1) {
+  for (int64_t row = row0; row < T; row += row_step, buf ^= 1) {
     const int64_t base = row * D;
     if (!kAhead) fetch(row);
     const float rr = r;
@@ -300,7 +320,7 @@ __global__ void __launch_bounds__(512)
     float dot = 0.f;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      const int c = (threadIdx.x + i * blockDim.x) * 8;
+      const int c = (threadIdx.x + i * step) * 8;
       if (c < D) {
         float wv[8];
         if constexpr (kAhead) {
@@ -323,15 +343,15 @@ __global__ void __launch_bounds__(512)
     if constexpr (kAhead) {
 #pragma unroll
       for (int i = 0; i < V; ++i) cd[i] = rd[i];
-      fetch(row + gridDim.x);
+      fetch(row + row_step);
     }
     // two buffers: a warp may still read this row's sums when another one
     // writes the next row's, never two rows on
-    dot = row_sum<false>(dot, red[buf]);
+    dot = row_sum<kWarp, kGroups>(dot, red[buf][kGroups ? threadIdx.y : 0]);
     const float k = rr * rr * (dot * inv_d);
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      const int c = (threadIdx.x + i * blockDim.x) * 8;
+      const int c = (threadIdx.x + i * step) * 8;
       if (c < D) {
         float d[8];
         if (dres_out) {
@@ -350,10 +370,23 @@ __global__ void __launch_bounds__(512)
       }
     }
   }
-  if (dw_part) {
+  if (kSeveral) {
+    if (!dw_part) return;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      const int c = (threadIdx.x + i * blockDim.x) * 8;
+      const int c = (threadIdx.x + i * step) * 8;
+      if (c < D) store8(group_dw + threadIdx.y * D + c, dw[i]);
+    }
+    __syncthreads();
+    for (int c = threadIdx.y * blockDim.x + threadIdx.x; c < D; c += blockDim.x * blockDim.y) {
+      float t = group_dw[c];
+      for (int i = 1; i < static_cast<int>(blockDim.y); ++i) t += group_dw[i * D + c];
+      dw_part[static_cast<int64_t>(blockIdx.x) * D + c] = t;
+    }
+  } else if (dw_part) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int c = (threadIdx.x + i * step) * 8;
       if (c < D) store8(dw_part + static_cast<int64_t>(blockIdx.x) * D + c, dw[i]);
     }
   }
@@ -449,30 +482,32 @@ template <typename XT, typename RT>
 cudaError_t add_rmsnorm_bwd(const void* dy, const void* dres_out, const void* s, int64_t T, int D,
                             const float* w, const float* rstd, void* dx, void* dres, float* dw,
                             float* ws, cudaStream_t stream) {
-  const int nvec = D / 8;
-  int V = 1;
-  while (nvec > V * 512 && V < 4) V *= 2;
-  const int threads = ((nvec + V - 1) / V + 31) / 32 * 32;
-  const int64_t grid = std::min<int64_t>({(T + 1) / 2, kNormBwdMaxParts,
-                                          static_cast<int64_t>(device_sm_count()) *
-                                              std::max(1, 1024 / threads)});
+  const RowShape sh = row_shape(D);
+  // Two rows or more per row's threads, up to 1024 threads per SM.
+  const int per_row = static_cast<int>(sh.block.x);
+  const int rows_at_once =
+      sh.warp ? kNormBwdWarps : sh.V > 1 ? 1 : std::max(1, std::min(kNormBwdGroups, 512 / per_row));
+  const int threads = per_row * rows_at_once;
+  const int64_t grid = std::min<int64_t>(
+      {(T + 2 * rows_at_once - 1) / (2 * rows_at_once), kNormBwdMaxParts,
+       static_cast<int64_t>(device_sm_count()) * std::max(1, 1024 / threads)});
+  const dim3 block(per_row, rows_at_once, 1);
   auto go = [&](auto kern) {
-    kern<<<static_cast<unsigned>(grid), threads, 0, stream>>>(
+    kern<<<static_cast<unsigned>(grid), block, 0, stream>>>(
         static_cast<const XT*>(dy), static_cast<const RT*>(dres_out), static_cast<const RT*>(s), T,
         D, w, rstd, static_cast<XT*>(dx), static_cast<RT*>(dres), dw ? ws : nullptr);
     return cudaGetLastError();
   };
   cudaError_t err;
-  switch (V) {
-    case 1:
-      err = go(add_rmsnorm_bwd_kernel<XT, RT, 1>);
-      break;
-    case 2:
-      err = go(add_rmsnorm_bwd_kernel<XT, RT, 2>);
-      break;
-    default:
-      err = go(add_rmsnorm_bwd_kernel<XT, RT, 4>);
-  }
+  if (sh.warp)
+    err = sh.V == 1 ? go(add_rmsnorm_bwd_kernel<XT, RT, 1, true, false>)
+                    : go(add_rmsnorm_bwd_kernel<XT, RT, 2, true, false>);
+  else if (rows_at_once > 1)
+    err = go(add_rmsnorm_bwd_kernel<XT, RT, 1, false, true>);
+  else
+    err = sh.V == 1   ? go(add_rmsnorm_bwd_kernel<XT, RT, 1, false, false>)
+          : sh.V == 2 ? go(add_rmsnorm_bwd_kernel<XT, RT, 2, false, false>)
+                      : go(add_rmsnorm_bwd_kernel<XT, RT, 4, false, false>);
   if (err != cudaSuccess || !dw) return err;
   dw_reduce_kernel<<<static_cast<unsigned>((D + 31) / 32), 1024, 0, stream>>>(
       ws, static_cast<int>(grid), D, dw);
