@@ -64,7 +64,9 @@ constexpr int64_t kSwapMaxRows = 1024;
 // In 8 bits, calls with at most this many routed rows per expert on average, as
 // measured (us, swap-AB against the pair kernel, K 2048, N 2048 unless stated):
 // 8 rows per expert of 8, K 4096: 12.7 / 18.4; 32 of 64, N 1024: 36 / 66; 64 of 8:
-// 14.9 / 15.1; 91 of 33, K and N 1024: 22.0 / 19.5; 128 of 8: 19.8 / 15.7.
+// 14.9 / 15.1; 91 of 33, K and N 1024: 22.0 / 19.5; 128 of 8: 19.8 / 15.7. Conv+Gate
+// at N 4096: 8 of 8: 25.2 / 31.3; 32 of 8: 27.7 / 32.4; 64 of 8: 34.3 / 33.3; 128 of
+// 8: 43.6 / 34.2.
 constexpr int64_t kSwapMaxRowsPerExpertQ8 = 64;
 
 struct Params {
@@ -556,15 +558,23 @@ __global__ void __launch_bounds__(PairGeo<MODE, kQ8>::kThreads, 1)
 // epilogue: out[token][n] = r * acc (bf16, k == 1) or per slot in float32.
 constexpr int SW_BM = 128;                     // weight rows per tile (MMA M)
 constexpr int SW_BN = 64;                      // tokens per tile (MMA N)
-constexpr int SW_STAGES = 8;
+constexpr int SW_MAX_STAGES = 8;
 constexpr int SW_A_BYTES = SW_BM * BK * 2;     // 16 KB of weights
 constexpr int SW_B_BYTES = SW_BN * BK * 2;     // 8 KB of tokens
-constexpr int SW_STAGE_BYTES = SW_A_BYTES + SW_B_BYTES;
-constexpr uint32_t SW_TMEM_COLS = 2 * SW_BN;
+// Conv+Gate (8-bit products only): a stage holds the tile's W_in and W_g rows
+// and an accumulator is u next to z, 64 tokens each.
+template <int MODE>
+struct SwapGeo {
+  static constexpr bool kGate = (MODE == kEpiGateH || MODE == kEpiGateSlots);
+  static constexpr int kStages = kGate ? 5 : SW_MAX_STAGES;
+  static constexpr int kStageBytes = (kGate ? 2 : 1) * SW_A_BYTES + SW_B_BYTES;
+  static constexpr int kAccCols = (kGate ? 2 : 1) * SW_BN;
+  static constexpr uint32_t kTmemCols = 2 * kAccCols;
+};
 
 struct SwapCtl {
-  uint64_t full[SW_STAGES];
-  uint64_t empty[SW_STAGES];
+  uint64_t full[SW_MAX_STAGES];
+  uint64_t empty[SW_MAX_STAGES];
   uint64_t tfull[2];
   uint64_t tempty[2];
   uint64_t drain;
@@ -575,7 +585,9 @@ struct SwapCtl {
   int tt[kMaxExperts];  // token tiles per expert
 };
 
-constexpr size_t kSwapSmemBytes = SW_STAGES * SW_STAGE_BYTES + sizeof(SwapCtl) + 1024;
+template <int MODE>
+constexpr size_t kSwapSmemBytes =
+    SwapGeo<MODE>::kStages * SwapGeo<MODE>::kStageBytes + sizeof(SwapCtl) + 1024;
 
 // Output row and router weight of one token of the tile, for the lane that
 // holds it (one token per lane, so the slot and weight loads of a chunk of
@@ -586,10 +598,13 @@ __device__ __forceinline__ void swap_token(const Params& p, int64_t prow, bool v
   orow = 0;
   r = 0.f;
   if (valid) {
-    const int slot = static_cast<int>(slot_of(p, prow));
-    r = p.topk_w ? p.topk_w[slot] : 1.f;  // no routing weights: r = 1
+    const int slot = MODE == kEpiGateH ? 0 : static_cast<int>(slot_of(p, prow));
+    // no routing weights: r = 1
+    r = !SwapGeo<MODE>::kGate && p.topk_w ? p.topk_w[slot] : 1.f;
     if (kQ8) r *= p.a_scale[prow];
-    orow = MODE == kEpiScaleToken ? slot / p.k : slot;
+    orow = MODE == kEpiGateH        ? static_cast<int>(prow)
+           : MODE == kEpiScaleToken ? slot / p.k
+                                    : slot;
   }
 }
 
@@ -604,7 +619,13 @@ __device__ __forceinline__ void swap_token(const Params& p, int64_t prow, bool v
 template <int MODE, bool kDense, bool kQ8>
 __global__ void __launch_bounds__(kThreads, 1)
     tc_swap_gemm_kernel(const __grid_constant__ CUtensorMap tmW,
+                        const __grid_constant__ CUtensorMap tmW1,
                         const __grid_constant__ CUtensorMap tmX, const Params p) {
+  constexpr bool kGate = SwapGeo<MODE>::kGate;
+  constexpr int SW_STAGES = SwapGeo<MODE>::kStages;
+  constexpr int SW_STAGE_BYTES = SwapGeo<MODE>::kStageBytes;
+  constexpr int kXOff = SW_STAGE_BYTES - SW_B_BYTES;  // the tokens' rows in a stage
+  constexpr int kAccCols = SwapGeo<MODE>::kAccCols;
   extern __shared__ uint8_t smem_raw[];
   // 1024-byte aligned base, kept as a shared-memory pointer (an offset into
   // the shared array, not an integer round-trip) so accesses stay LDS/STS.
@@ -636,7 +657,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tma_prefetch_desc(&tmX);
   }
   if (warp == 1) {
-    tmem_alloc(&ctl.tmem_base, SW_TMEM_COLS);
+    tmem_alloc(&ctl.tmem_base, SwapGeo<MODE>::kTmemCols);
     tmem_relinquish();
   }
   if (!kDense) {
@@ -694,7 +715,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             tma_load_5d(sa, &tmW, &ctl.full[stage], 0, 0, kb, w_blk, e);
           else
             tma_load_3d(sa, &tmW, &ctl.full[stage], kb * kBK<kQ8>, n0, e);
-          tma_load_2d(sa + SW_A_BYTES, &tmX, &ctl.full[stage], kb * kBK<kQ8>, r0);
+          if (kGate)
+            tma_load_3d(sa + SW_A_BYTES, &tmW1, &ctl.full[stage], kb * kBK<kQ8>, n0, e);
+          tma_load_2d(sa + kXOff, &tmX, &ctl.full[stage], kb * kBK<kQ8>, r0);
           issued |= 1u << stage;
           last_par = (last_par & ~(1u << stage)) | (phase << stage);
           if (++stage == SW_STAGES) {
@@ -718,7 +741,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int tile = blockIdx.x; tile < total && ok; tile += gridDim.x) {
         if (!mbar_wait(&ctl.tempty[acc], acc_phase ^ 1u, abort_flag, p.status)) break;
         tc_fence_after();
-        const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(acc * SW_BN);
+        const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(acc * kAccCols);
         for (int kb = 0; kb < KB; ++kb) {
           if (!mbar_wait(&ctl.full[stage], phase, abort_flag, p.status)) {
             ok = false;
@@ -726,7 +749,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           tc_fence_after();
           const uint32_t a_addr = smem_u32(smem + stage * SW_STAGE_BYTES);
-          const uint32_t b_addr = a_addr + SW_A_BYTES;
+          const uint32_t b_addr = a_addr + kXOff;
 #pragma unroll
           for (int kk = 0; kk < BKB / 32; ++kk) {
             const uint64_t da = sw128_kmajor_desc(a_addr + kk * 32);
@@ -735,6 +758,9 @@ __global__ void __launch_bounds__(kThreads, 1)
               mma_e4m3_ss(d_tmem, da, db, idesc, (kb | kk) != 0);
             else
               mma_bf16_ss(d_tmem, da, db, idesc, (kb | kk) != 0);
+            if constexpr (kGate)
+              mma_e4m3_ss(d_tmem + SW_BN, sw128_kmajor_desc(a_addr + SW_A_BYTES + kk * 32), db,
+                          idesc, (kb | kk) != 0);
           }
           mma_commit(&ctl.empty[stage]);
           if (++stage == SW_STAGES) {
@@ -793,18 +819,34 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!mbar_wait(&ctl.tfull[acc], acc_phase, abort_flag, p.status)) break;
       tc_fence_after();
       const uint32_t t_row =
-          tmem_base + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(acc * SW_BN);
+          tmem_base + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(acc * kAccCols);
       const int n = w_blk * SW_BM + q * 32 + lane;  // this thread's output column
       const float sw = kQ8 ? p.w0_scale[static_cast<int64_t>(e) * p.N + n] : 1.f;
+      const float sw1 = kGate ? p.w1_scale[static_cast<int64_t>(e) * p.N + n] : 1.f;
 #pragma unroll
       for (int c = 0; c < SW_BN / 32; ++c) {
         if (32 * c < nv) {  // warp-uniform
-          uint32_t a[32];
+          uint32_t a[32], z[kGate ? 32 : 1];
           tmem_ld32(t_row + c * 32, a);
+          if constexpr (kGate) tmem_ld32(t_row + SW_BN + c * 32, z);
           tmem_ld_wait();
 #pragma unroll
           for (int j = 0; j < 32; ++j) {
             if (32 * c + j < nv) {  // warp-uniform
+              if constexpr (kGate) {
+                const int64_t i =
+                    static_cast<int64_t>(__shfl_sync(0xffffffffu, orow[c], j)) * p.N + n;
+                const float sa = __shfl_sync(0xffffffffu, rw[c], j);
+                const float uv = __uint_as_float(a[j]) * (sa * sw);
+                const float zv = __uint_as_float(z[j]) * (sa * sw1);
+                if (MODE == kEpiGateH) {
+                  static_cast<__nv_bfloat16*>(p.out)[i] = __float2bfloat16_rn(silu_gate(uv, zv));
+                } else {
+                  static_cast<float*>(p.out)[i] = uv;
+                  static_cast<float*>(p.out)[p.R * p.N + i] = zv;
+                }
+                continue;
+              }
               const int o = __shfl_sync(0xffffffffu, orow[c], j);
               float v = __shfl_sync(0xffffffffu, rw[c], j) * __uint_as_float(a[j]);
               if (kQ8) v *= sw;
@@ -832,7 +874,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   if (warp == 1) {
     tc_fence_after();
-    tmem_dealloc(tmem_base, SW_TMEM_COLS);
+    tmem_dealloc(tmem_base, SwapGeo<MODE>::kTmemCols);
   }
 }
 
@@ -921,14 +963,18 @@ cudaError_t launch_grouped(int mode, const void* a_sorted, const float* a_scale,
   const bool gate = (mode == kEpiGateH || mode == kEpiGateSlots);
   const int tile_n = gate ? 128 : 256;
   // Few tokens (decode): the swap-AB kernel streams every weight tile once.
-  if (!gate && R <= (kQ8 ? kSwapMaxRowsPerExpertQ8 * E : kSwapMaxRows) && N % SW_BM == 0 && K % kAlign == 0 && E <= kMaxExperts) {
+  if ((kQ8 || !gate) && R <= (kQ8 ? kSwapMaxRowsPerExpertQ8 * E : kSwapMaxRows) &&
+      N % SW_BM == 0 && K % kAlign == 0 && E <= kMaxExperts) {
     if (R == 0) return cudaSuccess;
-    CUtensorMap tw, tx;
+    CUtensorMap tw, tw1, tx;
     if (!make_map<kQ8>(&tw, w0, K, N, E, SW_BM)) return cudaErrorInvalidValue;
+    tw1 = tw;
+    if (gate && !make_map<kQ8>(&tw1, w1, K, N, E, SW_BM)) return cudaErrorInvalidValue;
     if (!make_map<kQ8>(&tx, a_sorted, K, R, 0, SW_BN)) return cudaErrorInvalidValue;
     Params p{};
     p.a_scale = a_scale;
     p.w0_scale = w0_scale;
+    p.w1_scale = w1_scale;
     p.offsets = offsets;
     p.sorted_slot = sorted_slot;
     p.topk_w = topk_w;
@@ -949,8 +995,16 @@ cudaError_t launch_grouped(int mode, const void* a_sorted, const float* a_scale,
     const int grid = static_cast<int>(std::min<int64_t>(sms, (tiles_ub + per_cta - 1) / per_cta));
     auto kern = (mode == kEpiScaleToken) ? tc_swap_gemm_kernel<kEpiScaleToken, false, kQ8>
                                          : tc_swap_gemm_kernel<kEpiScaleSlots, false, kQ8>;
+    size_t smem = kSwapSmemBytes<kEpiScaleToken>;
+    if constexpr (kQ8) {
+      if (gate) {
+        kern = (mode == kEpiGateH) ? tc_swap_gemm_kernel<kEpiGateH, false, true>
+                                   : tc_swap_gemm_kernel<kEpiGateSlots, false, true>;
+        smem = kSwapSmemBytes<kEpiGateH>;
+      }
+    }
     cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                           static_cast<int>(kSwapSmemBytes));
+                                           static_cast<int>(smem));
     if (err != cudaSuccess) return err;
     // Programmatic dependent launch: the set-up runs
     // while the kernel before (the dispatch) finishes.
@@ -960,11 +1014,11 @@ cudaError_t launch_grouped(int mode, const void* a_sorted, const float* a_scale,
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(grid), 1, 1);
     cfg.blockDim = dim3(kThreads, 1, 1);
-    cfg.dynamicSmemBytes = kSwapSmemBytes;
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kern, tw, tx, p);
+    return cudaLaunchKernelEx(&cfg, kern, tw, tw1, tx, p);
   }
   if (K % kAlign != 0 || N % 128 != 0 || E > kMaxExperts || R >= (int64_t(1) << 31))
     return cudaErrorInvalidValue;
@@ -1097,7 +1151,7 @@ cudaError_t launch_tc_dense_small(int mode, const void* x, int64_t T, int K, con
   auto kern = (mode == kEpiScaleToken) ? tc_swap_gemm_kernel<kEpiScaleToken, true, false>
                                        : tc_swap_gemm_kernel<kEpiScaleSlots, true, false>;
   cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         static_cast<int>(kSwapSmemBytes));
+                                         static_cast<int>(kSwapSmemBytes<kEpiScaleToken>));
   if (err != cudaSuccess) return err;
   // a programmatic dependent of the router: the weight streaming and the
   // MMAs run while the router finishes; the epilogue waits for it
@@ -1107,11 +1161,11 @@ cudaError_t launch_tc_dense_small(int mode, const void* x, int64_t T, int K, con
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(grid), 1, 1);
   cfg.blockDim = dim3(kThreads, 1, 1);
-  cfg.dynamicSmemBytes = kSwapSmemBytes;
+  cfg.dynamicSmemBytes = kSwapSmemBytes<kEpiScaleToken>;
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kern, tw, tx, p);
+  return cudaLaunchKernelEx(&cfg, kern, tw, tw, tx, p);
 }
 
 }  // namespace rom
