@@ -21,10 +21,11 @@
 //   Out / in-projection: 256 output columns, scaled by r in the epilogue (a
 //   last tile of 128 columns when N % 256 == 128: the weight rows past N are
 //   zero-filled by TMA and those columns are not stored).
-// CTA: persistent (one pair of CTAs per pair of SMs), 6 warps:
+// CTA: persistent (one pair of CTAs per pair of SMs), 6 warps (10 in 8 bits):
 //   warp 0  TMA producer (one thread), 6- or 7-stage ring (32 KB/stage/CTA)
 //   warp 1  TMEM allocator; in CTA 0 also the MMA issuer (one thread)
-//   warps 2-5  epilogue; warp w reads TMEM lanes 32*(w%4) .. +31
+//   warps 2-5  epilogue; warp w reads TMEM lanes 32*(w%4) .. +31 (in 8 bits,
+//              where a tile's MMAs take half the time, warps 2-9: two per lane group)
 // Two TMEM accumulators (2 x 256 columns) let the epilogue of one tile run
 // while the MMAs of the next tile proceed. Every wait is bounded.
 // Few routed rows (decode) take a swap-AB kernel instead (below).
@@ -554,8 +555,9 @@ __global__ void __launch_bounds__(PairGeo<MODE, kQ8>::kThreads, 1)
 // E x N/128 x ceil(n_e / 64) -- enough tiles to cover the SMs even when every
 // expert has only a handful of tokens. The kernel is bound by HBM, not by
 // the SM count, so the grid is sized to give every CTA the same number of
-// tiles (320 tiles: 107 CTAs of 3 tiles, not 148 CTAs and a partial wave). Same output as the Out / in-projection
-// epilogue: out[token][n] = r * acc (bf16, k == 1) or per slot in float32.
+// tiles (320 tiles: 107 CTAs of 3 tiles, not 148 CTAs and a partial wave). Same
+// output as the Out / in-projection epilogue: out[token][n] = r * acc (bf16,
+// k == 1) or per slot in float32; in 8 bits also Conv+Gate's.
 constexpr int SW_BM = 128;                     // weight rows per tile (MMA M)
 constexpr int SW_BN = 64;                      // tokens per tile (MMA N)
 constexpr int SW_MAX_STAGES = 8;

@@ -90,6 +90,7 @@ CASES = [
     # both sides of the 64 rows per expert at which the kernels change
     (256, 144, 128, 4, 1, None), (257, 144, 128, 4, 1, None), (33, 96, 128, 2, 2, 1),
     (1300, 160, 256, 4, 1, 2), (2, 16, 128, 1, 1, None), (300, 2048, 640, 3, 2, None),
+    (250, 144, 384, 4, 1, 3),  # few rows, several token tiles of one expert
 ]
 
 
