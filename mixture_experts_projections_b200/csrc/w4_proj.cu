@@ -66,6 +66,7 @@ struct W4Params {
   int nt, kb;           // 16-row tiles, 128-column blocks
   int splits;           // CTAs of a cluster that share a row block's columns
   int max_active;       // upper bound of the experts in use
+  int passes;           // CTAs that share an expert's passes over its tokens
   int stages;           // of the ring
   int to_token;         // bf16 rows in token order (k == 1), else float32 slot rows
   int* status;
@@ -263,6 +264,8 @@ __global__ void __maxnreg__(96)
     }
     count += n;
   }
+  const int first = blockIdx.z * kTok;
+  if (first >= count) return;  // cluster-uniform
   __syncthreads();
   volatile int* abort_flag = &ctl.abort;
 
@@ -274,7 +277,7 @@ __global__ void __maxnreg__(96)
   int stage = 0;
   uint32_t phase = 0;
 
-  for (int p0 = 0; p0 < count; p0 += kTok) {
+  for (int p0 = first; p0 < count; p0 += gridDim.z * kTok) {
     const int n_tok = min(kTok, count - p0);
     const int n_blk = (n_tok + 7) / 8;
     float acc[NB][4];
@@ -450,7 +453,8 @@ cudaError_t launch_w4(W4Params p, const W4Maps& maps, int warps, int mats, cudaS
   attr[1].val.clusterDim.z = 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(row_blks * p.splits),
-                     static_cast<unsigned>(p.max_active * mats), 1);
+                     static_cast<unsigned>(p.max_active * mats),
+                     static_cast<unsigned>(p.passes));
   cfg.blockDim = dim3(static_cast<unsigned>((warps + 1) * 32), 1, 1);
   cfg.dynamicSmemBytes = static_cast<size_t>(p.stages) * stage + sizeof(W4Ctl);
   cfg.stream = stream;
@@ -579,28 +583,36 @@ cudaError_t launch_w4_proj(const void* x, int T, int K, const void* q0, const vo
   const double most = std::min(static_cast<double>(T), even + 2.0 * std::sqrt(even));
   const int nb = most <= 8.0 ? 1 : most <= 16.0 ? 2 : 3;
   // Shape of the work: CTAs of `warps` 16-row tiles, `splits` of them (a
-  // cluster) sharing the columns of one row block. The cost is an SM's: the
-  // tiles that its CTAs' warps go through, ceil(CTAs / SMs) * warps / splits,
-  // slower where few warps are resident and where CTAs start late, plus the
-  // cluster's hand-over of its sums (1.5 tiles of 4096 columns per split).
-  // Measured, us, at 4 experts of 10240 x 4096: one token 10.9 (9 warps, 2
-  // splits; 12.6 with 4 and 1, 14.0 with 9 and 4), 4 tokens 14.2 (9 and 2; 15.0
-  // with 5 and 1), 64 tokens 36.3 (9 and 1; 44 with 5, 47 with 8).
-  const double used = E * (1.0 - std::pow(1.0 - static_cast<double>(k) / E, T));
+  // cluster) sharing the columns of one row block, `passes` sharing an expert's
+  // token blocks where it has more than nb. The cost is an SM's: the CTAs that
+  // come to it times what one goes through, its warps' 16 x 128 tiles, dearer
+  // where few warps are resident, and the cluster's hand-over of its sums, in
+  // tiles (fewer where a tile takes longer for its tokens). The constants are the
+  // best of a grid over 75 shapes timed in every form, 3 % above the best form on
+  // average, geometrically. Measured, us, at 4 experts of 10240 x 4096: one token
+  // 10.7 (9 warps, 2 splits; 12.6 with 4 and 1, 14.0 with 9 and 4), 64 tokens 36.3
+  // (9 and 1; 44 with 5, 47 with 8); 4 experts of 154 x 3960, 30 tokens, top-3: 9.3
+  // (4 and 8; 14.2 with 4 and 2).
+  const double used = std::ceil(E * (1.0 - std::pow(1.0 - static_cast<double>(k) / E, T)) - 0.1);
+  const double blocks = std::max(1.0, static_cast<double>(T) * k / used / 8.0);
+  const double hand_over = 96.0 / std::sqrt(blocks);
+  const int passes = std::max(1, static_cast<int>(std::ceil(blocks / nb - 0.1)));
   const int sms = device_sm_count();
   int warps = kW4MaxWarps;
   double best = 1e30;
-  for (int s = 1; s <= 8 && (s == 1 || p.kb / s >= 4); s *= 2) {
-    for (int w = kW4MaxWarps; w >= kW4MinWarps; --w) {
-      const double ctas = std::ceil(std::ceil(((p.nt + w - 1) / w) * used * mats * s) / sms);
-      const int room = w4_resident(nb, w);
-      const double resident = std::min(ctas, static_cast<double>(room)) * w;
-      const double cost = ctas * w / s * (1.0 + 6.0 / resident) * (ctas > room ? 1.1 : 1.0) +
-                          (s > 1 ? 1.5 * s * 32.0 / p.kb : 0.0);
-      if (cost < best * 0.999) {
-        best = cost;
-        warps = w;
-        p.splits = s;
+  for (int z = 1; z <= passes; z = z < passes ? passes : passes + 1) {
+    for (int s = 1; s <= 8 && s <= p.kb; s *= 2) {
+      for (int w = kW4MaxWarps; w >= kW4MinWarps; --w) {
+        const double ctas = std::ceil(((p.nt + w - 1) / w) * used * mats * s * z / sms);
+        const double resident = std::min(ctas, static_cast<double>(w4_resident(nb, w))) * w;
+        const double tiles = w * ((p.kb + s - 1) / s) * (1.0 + 11.0 / resident);
+        const double cost = ctas * passes / z * (tiles + (s > 1 ? hand_over : 0.0));
+        if (cost < best * 0.999) {
+          best = cost;
+          warps = w;
+          p.splits = s;
+          p.passes = z;
+        }
       }
     }
   }

@@ -29,7 +29,7 @@ def lib():
     (dict(k=3, E=2), 1), (dict(k=9, E=16), 1), (dict(group=16), 1), (dict(group=0), 1), (dict(x=None), 1),
     (dict(q0=None), 1), (dict(s0=None), 1), (dict(topk_idx=None), 1), (dict(topk_w=None), 1), (dict(out=None), 1),
     (dict(q1=FAKE), 1), (dict(proj=4, q1=FAKE), 1), (dict(proj=4), 1),
-    (dict(T=65), 2), (dict(K=60), 2), (dict(x=ctypes.c_void_p((1 << 20) + 8)), 2),
+    (dict(T=65), 2), (dict(K=60), 2), (dict(K=1500), 2), (dict(x=ctypes.c_void_p((1 << 20) + 8)), 2),
     (dict(s0=ctypes.c_void_p((1 << 20) + 2)), 2), (dict(out=ctypes.c_void_p((1 << 20) + 1)), 2),
     (dict(k=2, out=ctypes.c_void_p((1 << 20) + 2)), 2),
 ])
@@ -118,6 +118,9 @@ CASES = [
     # columns shared by a cluster, once over the tokens and (all 64 on one expert) several times
     (3, 8192, 16, 1, 1, 64, None), (64, 4096, 130, 4, 1, 128, 2), (40, 2048, 20, 16, 2, 32, 3),
     (64, 768, 140, 4, 1, 128, 2), (33, 8, 8, 2, 2, 32, None), (40, 1160, 129, 2, 1, 128, 0),
+    # an expert's passes shared by CTAs, with and without shared columns; fewer blocks of columns than CTAs of a cluster
+    (60, 1504, 200, 1, 1, 64, None), (64, 264, 70, 2, 2, 32, None), (41, 72, 2500, 1, 1, 128, None),
+    (20, 640, 20, 4, 1, 64, None),
 ]
 
 
