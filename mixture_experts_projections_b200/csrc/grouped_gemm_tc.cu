@@ -95,13 +95,13 @@ struct Params {
 };
 
 // 8-bit products: acc[j] *= sa * sw[j] for 32 columns, the scales of the
-// columns read as 8 uniform 16-byte loads.
+// columns read from shared memory as 8 uniform 16-byte loads.
 template <bool kQ8>
 __device__ __forceinline__ void apply_scales(uint32_t (&acc)[32], float sa, const float* sw) {
   if (kQ8) {
 #pragma unroll
     for (int v = 0; v < 8; ++v) {
-      const float4 s = __ldg(reinterpret_cast<const float4*>(sw) + v);
+      const float4 s = reinterpret_cast<const float4*>(sw)[v];
       acc[4 * v + 0] = __float_as_uint(__uint_as_float(acc[4 * v + 0]) * (sa * s.x));
       acc[4 * v + 1] = __float_as_uint(__uint_as_float(acc[4 * v + 1]) * (sa * s.y));
       acc[4 * v + 2] = __float_as_uint(__uint_as_float(acc[4 * v + 2]) * (sa * s.z));
@@ -140,14 +140,57 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
 // float32 outputs (per-slot partials) go row by row through the warp's
 // staging tile `stg` (row-coalesced stores); the bf16 rows, half as wide,
 // are stored directly in 16-byte pieces, which measured faster for them.
+// What a tile's row needs besides its accumulator: its slot, routing weight (or
+// 1) and scale, and of a lane the scales of up to 128 columns (four of its own:
+// of the chunks' columns, and of W_g's behind W_in's for the gate modes).
+struct EpiRow {
+  int64_t slot = 0;
+  float r = 0.f, sa = 0.f, sw[4] = {0.f, 0.f, 0.f, 0.f};
+};
+template <int MODE, bool kQ8>
+__device__ __forceinline__ EpiRow epilogue_row(const Params& p, bool valid, int64_t prow, int e,
+                                               int n0, int c0, int c1) {
+  EpiRow o;
+  if (valid) {
+    if (MODE != kEpiGateH) o.slot = slot_of(p, prow);
+    if (kQ8) o.sa = p.a_scale[prow];
+    // no routing weights passed: r = 1
+    if (MODE == kEpiScaleToken || MODE == kEpiScaleSlots) o.r = p.topk_w ? p.topk_w[o.slot] : 1.f;
+  }
+  if (kQ8) {
+    constexpr bool kGate = (MODE == kEpiGateH || MODE == kEpiGateSlots);
+    const int64_t at = static_cast<int64_t>(e) * p.N;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int c = c0 + (kGate ? i & 1 : i), n = n0 + c * 32 + (threadIdx.x & 31);
+      if (c < c1 && n < p.N) o.sw[i] = (kGate && i > 1 ? p.w1_scale : p.w0_scale)[at + n];
+    }
+  }
+  return o;
+}
+
 template <int MODE, bool kQ8>
 __device__ __forceinline__ void epilogue_rows(const Params& p, uint32_t t_row, bool valid,
-                                              int64_t prow, int e, int n0, int w, int c0, int c1,
-                                              float* stg) {
-  // this row's scale and the tile's columns' (8-bit products)
-  const float sa = kQ8 && valid ? p.a_scale[prow] : 0.f;
-  const float* sw0 = kQ8 ? p.w0_scale + static_cast<int64_t>(e) * p.N + n0 : nullptr;
-  const float* sw1 = kQ8 && p.w1_scale ? p.w1_scale + static_cast<int64_t>(e) * p.N + n0 : nullptr;
+                                              int64_t prow, const EpiRow& own, int n0, int w,
+                                              int c0, int c1, float* stg, float* sws) {
+  const float sa = own.sa;
+  // the output rows that this lane stores from the staging tile
+  constexpr bool kF32 = (MODE == kEpiGateSlots || MODE == kEpiScaleSlots);
+  int rows[8];
+  if (kF32 || kQ8) {
+    const int64_t row = MODE == kEpiGateH        ? prow
+                        : MODE == kEpiScaleToken ? own.slot / p.k
+                                                 : own.slot;
+    const int mine = valid ? static_cast<int>(row) : -1, lane = threadIdx.x & 31;
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      rows[i] = __shfl_sync(0xffffffffu, mine, kF32 ? 4 * i + (lane >> 3) : (8 * i + (lane >> 2)) & 31);
+  }
+  if (kQ8) {  // the columns' scales, 32 of a chunk in a row
+#pragma unroll
+    for (int i = 0; i < 4; ++i) sws[i * 32 + (threadIdx.x & 31)] = own.sw[i];
+    __syncwarp();
+  }
   if (MODE == kEpiGateH) {
     __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out);
 #pragma unroll 1
@@ -156,8 +199,8 @@ __device__ __forceinline__ void epilogue_rows(const Params& p, uint32_t t_row, b
       tmem_ld32(t_row + c * 32, u);
       tmem_ld32(t_row + w + c * 32, z);
       tmem_ld_wait();
-      apply_scales<kQ8>(u, sa, sw0 + c * 32);
-      apply_scales<kQ8>(z, sa, sw1 + c * 32);
+      apply_scales<kQ8>(u, sa, sws + (c - c0) * 32);
+      apply_scales<kQ8>(z, sa, sws + (c - c0) * 32 + 64);
       if (valid || kQ8) {
         uint4* dst = reinterpret_cast<uint4*>(out + prow * p.N + n0 + c * 32);
         uint4 ws[4];
@@ -177,39 +220,38 @@ __device__ __forceinline__ void epilogue_rows(const Params& p, uint32_t t_row, b
           else
             dst[v] = w;
         }
-        if (kQ8) store_rows_bf16(reinterpret_cast<uint8_t*>(stg), ws, valid ? dst : nullptr);
+        if (kQ8)
+          store_tile_bf16(reinterpret_cast<uint8_t*>(stg), ws, rows, out + n0 + c * 32, p.N);
       }
     }
   } else if (MODE == kEpiGateSlots) {
     float* out = static_cast<float*>(p.out);
-    const int64_t slot = valid ? slot_of(p, prow) : 0;
 #pragma unroll 1
     for (int c = c0; c < c1; ++c) {
       uint32_t u[32], z[32];
       tmem_ld32(t_row + c * 32, u);
       tmem_ld32(t_row + w + c * 32, z);
       tmem_ld_wait();
-      apply_scales<kQ8>(u, sa, sw0 + c * 32);
-      apply_scales<kQ8>(z, sa, sw1 + c * 32);
+      apply_scales<kQ8>(u, sa, sws + (c - c0) * 32);
+      apply_scales<kQ8>(z, sa, sws + (c - c0) * 32 + 64);
       float f[32];
 #pragma unroll
       for (int j = 0; j < 32; ++j) f[j] = __uint_as_float(u[j]);
-      store_rows_f32(stg, f, valid ? out + slot * p.N + n0 + c * 32 : nullptr);
+      store_tile_f32(stg, f, rows, out + n0 + c * 32, p.N);
 #pragma unroll
       for (int j = 0; j < 32; ++j) f[j] = __uint_as_float(z[j]);
-      store_rows_f32(stg, f, valid ? out + (p.R + slot) * p.N + n0 + c * 32 : nullptr);
+      store_tile_f32(stg, f, rows, out + p.R * p.N + n0 + c * 32, p.N);
     }
   } else {
-    const int64_t slot = valid ? slot_of(p, prow) : 0;
-    // no routing weights passed: r = 1
-    const float r = valid ? (p.topk_w ? p.topk_w[slot] : 1.f) : 0.f;
+    const int64_t slot = own.slot;
+    const float r = own.r;
 #pragma unroll 1
     for (int c = c0; c < c1; ++c) {
       if (n0 + c * 32 >= p.N) break;  // partial last tile (N % 256 == 128)
       uint32_t a[32];
       tmem_ld32(t_row + c * 32, a);
       tmem_ld_wait();
-      apply_scales<kQ8>(a, sa, sw0 + c * 32);
+      apply_scales<kQ8>(a, sa, sws + (c - c0) * 32);
       if (MODE == kEpiScaleToken) {
         if (valid || kQ8) {
           __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out);
@@ -227,14 +269,15 @@ __device__ __forceinline__ void epilogue_rows(const Params& p, uint32_t t_row, b
             else
               dst[v] = w;
           }
-          if (kQ8) store_rows_bf16(reinterpret_cast<uint8_t*>(stg), ws, valid ? dst : nullptr);
+          if (kQ8)
+            store_tile_bf16(reinterpret_cast<uint8_t*>(stg), ws, rows, out + n0 + c * 32, p.N);
         }
       } else {
         float f[32];
 #pragma unroll
         for (int j = 0; j < 32; ++j) f[j] = r * __uint_as_float(a[j]);
         float* out = static_cast<float*>(p.out);
-        store_rows_f32(stg, f, valid ? out + slot * p.N + n0 + c * 32 : nullptr);
+        store_tile_f32(stg, f, rows, out + n0 + c * 32, p.N);
       }
     }
   }
@@ -272,6 +315,8 @@ struct PairGeo {
   static constexpr int kStages = (kF32 ? 6 : 7) - (kQ8 ? 1 : 0);
   static constexpr int kStageTile =  // bytes per epilogue warp
       kF32 ? kStageFloats * 4 : kQ8 ? kStageBf16Bytes : 0;
+  // bytes of its columns' scales, behind it
+  static constexpr int kScales = kQ8 ? 512 : 0;
   static constexpr int kThreads = 64 + 32 * kEpiWarps;
 };
 constexpr int P_A_BYTES = BM * BK * 2;       // 16 KB: this CTA's 128 rows
@@ -296,7 +341,8 @@ constexpr size_t kPairCtlBytes = (sizeof(PairCtl) + 15) / 16 * 16;
 template <int MODE, bool kQ8>
 constexpr size_t pair_smem_bytes() {
   using Geo = PairGeo<MODE, kQ8>;
-  return Geo::kStages * P_STAGE_BYTES + kPairCtlBytes + Geo::kEpiWarps * Geo::kStageTile + 1024;
+  return Geo::kStages * P_STAGE_BYTES + kPairCtlBytes + Geo::kEpiWarps * (Geo::kStageTile + Geo::kScales) +
+         1024;
 }
 
 template <int MODE, bool kQ8>
@@ -508,31 +554,55 @@ __global__ void __launch_bounds__(PairGeo<MODE, kQ8>::kThreads, 1)
     constexpr int kParts = kEpiWarps / 4;
     const uint32_t tempty0 = mapa_shared(smem_u32(&ctl.tempty[0]), 0);
     float* stg = reinterpret_cast<float*>(smem + P_STAGES * P_STAGE_BYTES + kPairCtlBytes +
-                                          (warp - 2) * PairGeo<MODE, kQ8>::kStageTile);
+                                          (warp - 2) * (PairGeo<MODE, kQ8>::kStageTile +
+                                                        PairGeo<MODE, kQ8>::kScales));
+    float* sws = stg + PairGeo<MODE, kQ8>::kStageTile / 4;
     int acc = 0;
     uint32_t acc_phase = 0;
-    int tile, half;
-    for (int j = 0; item(j, tile, half); ++j) {
+    // An item's rows and columns for this warp.
+    struct Part {
+      bool valid;
+      int64_t prow;
+      int n0, w, c0, c1;
+      EpiRow own;
+    };
+    auto part_of = [&](int tile, int half) {
+      Part o;
       int e, m_blk, n_blk;
       coords(tile, e, m_blk, n_blk);
+      const int row_local = m_blk * PM + static_cast<int>(rank) * BM + q * 32 + lane;
+      o.valid = row_local < ctl.off[e + 1] - ctl.off[e];
+      o.prow = static_cast<int64_t>(ctl.off[e]) + row_local;
+      o.w = half < 0 ? kTileN : kTileN / 2;
+      o.n0 = n_blk * kTileN + (half < 0 ? 0 : half * o.w);
+      o.c0 = part * (o.w / 32) / kParts;
+      o.c1 = (part + 1) * (o.w / 32) / kParts;
+      o.own = epilogue_row<MODE, kQ8>(p, o.valid, o.prow, e, o.n0, o.c0, o.c1);
+      return o;
+    };
+    // In 8 bits the next item's slots, weights and scales are on their way while
+    // this item's accumulator is stored.
+    int tile, half;
+    Part next;
+    if (kQ8 && item(0, tile, half)) next = part_of(tile, half);
+    for (int j = 0; item(j, tile, half); ++j) {
+      Part cur;
+      if (kQ8) cur = next;
+      else cur = part_of(tile, half);
       if (!mbar_wait(&ctl.tfull[acc], acc_phase, abort_flag, p.status)) break;
       tc_fence_after();
-      const int row_local = m_blk * PM + static_cast<int>(rank) * BM + q * 32 + lane;
-      const bool valid = row_local < ctl.off[e + 1] - ctl.off[e];
-      const int64_t prow = static_cast<int64_t>(ctl.off[e]) + row_local;
+      if (kQ8 && item(j + 1, tile, half)) next = part_of(tile, half);
       const uint32_t t_row =
           tmem_base + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(acc * UMMA_N);
-      const int w = half < 0 ? kTileN : kTileN / 2;
-      epilogue_rows<MODE, kQ8>(p, t_row, valid, prow, e,
-                               n_blk * kTileN + (half < 0 ? 0 : half * w), w,
-                               part * (w / 32) / kParts, (part + 1) * (w / 32) / kParts, stg);
+      epilogue_rows<MODE, kQ8>(p, t_row, cur.valid, cur.prow, cur.own, cur.n0, cur.w, cur.c0,
+                               cur.c1, stg, sws);
       tc_fence_before();
       __syncwarp();
       if (lane == 0) {
         if (leader)
           mbar_arrive(&ctl.tempty[acc]);
         else
-          mbar_arrive_remote(tempty0 + static_cast<uint32_t>(acc * sizeof(uint64_t)));
+          mbar_arrive_remote_relaxed(tempty0 + static_cast<uint32_t>(acc * sizeof(uint64_t)));
       }
       acc ^= 1;
       if (acc == 0) acc_phase ^= 1u;

@@ -336,24 +336,52 @@ __device__ __forceinline__ void store_rows_f32(float* stg, const float (&v)[32],
   __syncwarp();
 }
 
-// The same for 32 columns of bf16, 16 bytes of `v` per 8 columns: eight rows of
-// 64 consecutive bytes per instruction. Rows 80 bytes apart in the staging tile.
-constexpr int kStageBf16Bytes = 32 * 80;  // per warp
-
-__device__ __forceinline__ void store_rows_bf16(uint8_t* stg, const uint4 (&v)[4], void* row) {
+// The same for a lane that knows which rows it stores: rows[i] is the output row
+// of the tile's row 4 i + lane / 8 (< 0: not stored), base the first of the 32
+// columns in output row 0. Four reads of the tile go out before their stores.
+__device__ __forceinline__ void store_tile_f32(float* stg, const float (&v)[32],
+                                               const int (&rows)[8], float* base, int N) {
   const int lane = threadIdx.x & 31;
-  uint4* s4 = reinterpret_cast<uint4*>(stg + lane * 80);
+  stage_block(stg, v);
+  base += (lane & 7) * 4;
 #pragma unroll
-  for (int j = 0; j < 4; ++j) s4[j] = v[j];
+  for (int h = 0; h < 8; h += 4) {
+    float4 x[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      x[i] = *reinterpret_cast<const float4*>(stg + (4 * (h + i) + (lane >> 3)) * kStagePitch +
+                                              (lane & 7) * 4);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (rows[h + i] >= 0)
+        *reinterpret_cast<float4*>(base + static_cast<int64_t>(rows[h + i]) * N) = x[i];
+  }
   __syncwarp();
+}
+
+// The same for 32 columns of bf16, 16 bytes of `v` per 8 columns: eight rows of
+// 64 consecutive bytes per instruction, rows[i] that of the tile's row 8 i +
+// lane / 4. The tile's rows are 64 bytes apart and their four pieces permuted by
+// the row's pair (conflict-free both ways).
+constexpr int kStageBf16Bytes = 32 * 64;  // per warp
+
+__device__ __forceinline__ void store_tile_bf16(uint8_t* stg, const uint4 (&v)[4],
+                                                const int (&rows)[8], __nv_bfloat16* base, int N) {
+  const int lane = threadIdx.x & 31;
+  uint4* s4 = reinterpret_cast<uint4*>(stg);
+#pragma unroll
+  for (int j = 0; j < 4; ++j) s4[lane * 4 + (j ^ ((lane >> 1) & 3))] = v[j];
+  __syncwarp();
+  base += (lane & 3) * 8;
+  uint4 x[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const int r = 8 * i + (lane >> 2), c = lane & 3;
-    uint4* dst = reinterpret_cast<uint4*>(
-        __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(row), r));
-    const uint4 x = reinterpret_cast<const uint4*>(stg + r * 80)[c];
-    if (dst) dst[c] = x;
+    const int r = 8 * i + (lane >> 2);
+    x[i] = s4[r * 4 + ((lane & 3) ^ ((r >> 1) & 3))];
   }
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    if (rows[i] >= 0) *reinterpret_cast<uint4*>(base + static_cast<int64_t>(rows[i]) * N) = x[i];
   __syncwarp();
 }
 
@@ -424,6 +452,14 @@ __device__ __forceinline__ bool mbar_wait_cluster(uint64_t* bar, uint32_t parity
 // in the peer CTA).
 __device__ __forceinline__ void mbar_arrive_remote(uint32_t cluster_addr) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr)
+               : "memory");
+}
+
+// The same to hand back a TMEM accumulator, whose reads have completed in every
+// lane (tcgen05.wait::ld, fence before the thread synchronisation): no memory of
+// the warp's is released, so the arrival does not wait for its stores.
+__device__ __forceinline__ void mbar_arrive_remote_relaxed(uint32_t cluster_addr) {
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr)
                : "memory");
 }
 
