@@ -34,9 +34,8 @@ namespace rom {
 namespace {
 
 constexpr float kE4m3Max = 448.0f;
-// Rows that a CTA of the backward goes through at a time: 8 of a warp each, or 4
-// to 2 of up to 1024 to 2048 columns.
-constexpr int kNormBwdWarps = 8;
+// Rows of 520 to 2048 columns that a CTA of the backward goes through at a time:
+// as many as 512 threads hold, up to this many (of shorter rows, 8 warps' worth).
 constexpr int kNormBwdGroups = 4;
 constexpr float kAmaxFloor = 7.888609052210118e-31f;  // 2^-100
 
@@ -102,16 +101,17 @@ __device__ __forceinline__ float as_stored(float v, const __nv_bfloat16*) {
   return __bfloat162float(__float2bfloat16_rn(v));
 }
 
-// A row's threads: one warp (kWarp; blockDim = (32, rows)), the whole CTA, or
+// A row's threads: kLanes of a warp (8, 16 or 32; blockDim = (kLanes, rows)), the
+// whole CTA (0), or
 // (kGroups) one of its blockDim.y groups with a named barrier each. Sums and
 // maxima over them come back in every thread; the order of the additions is
 // fixed. `red` holds one value per warp and is written once per kernel (or
 // between barriers of the caller).
-template <bool kWarp, bool kGroups = false>
+template <int kLanes, bool kGroups = false>
 __device__ __forceinline__ float row_sum(float v, float* red) {
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  if (kWarp) return v;
+  for (int o = (kLanes ? kLanes : 32) / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  if (kLanes) return v;
   const int warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
   if ((threadIdx.x & 31) == 0) red[warp] = v;
   if (kGroups)
@@ -122,10 +122,15 @@ __device__ __forceinline__ float row_sum(float v, float* red) {
   for (int i = 0; i < nw; ++i) s += red[i];
   return s;
 }
-template <bool kWarp>
+template <int kLanes>
 __device__ __forceinline__ uint32_t row_max(uint32_t v, uint32_t* red) {
-  v = __reduce_max_sync(0xffffffffu, v);
-  if (kWarp) return v;
+  if (kLanes == 0 || kLanes == 32) {
+    v = __reduce_max_sync(0xffffffffu, v);
+  } else {
+#pragma unroll
+    for (int o = kLanes / 2; o > 0; o >>= 1) v = max(v, __shfl_xor_sync(0xffffffffu, v, o));
+  }
+  if (kLanes) return v;
   const int warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
   if ((threadIdx.x & 31) == 0) red[warp] = v;
   __syncthreads();
@@ -162,7 +167,7 @@ __device__ __forceinline__ void store_codes(uint8_t* p, const float (&v)[8], flo
   *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
 }
 
-template <typename XT, typename RT, int V, bool kWarp>
+template <typename XT, typename RT, int V, int kLanes>
 __global__ void __launch_bounds__(512)
     add_rmsnorm_kernel(const XT* x, const RT* res, int64_t T, int D,
                                    const float* __restrict__ w, float eps, RT* res_out, XT* y,
@@ -171,16 +176,16 @@ __global__ void __launch_bounds__(512)
   __shared__ float red[32];
   __shared__ uint32_t redm[32];
   const int64_t row =
-      kWarp ? blockIdx.x * static_cast<int64_t>(blockDim.y) + threadIdx.y : blockIdx.x;
-  if (kWarp && row >= T) return;
-  const int step = kWarp ? 32 : blockDim.x;
+      kLanes ? blockIdx.x * static_cast<int64_t>(blockDim.y) + threadIdx.y : blockIdx.x;
+  const int cols = kLanes && row >= T ? 0 : D;  // no row: no columns
+  const int step = kLanes ? kLanes : blockDim.x;
   const int64_t base = row * D;
   float s[V][8];
   float sum = 0.f;
 #pragma unroll
   for (int i = 0; i < V; ++i) {
     const int c = (threadIdx.x + i * step) * 8;
-    if (c < D) {
+    if (c < cols) {
       load8(x + base + c, s[i]);
       if (res) {
         float r[8];
@@ -195,14 +200,14 @@ __global__ void __launch_bounds__(512)
       }
     }
   }
-  sum = row_sum<kWarp>(sum, red);
+  sum = row_sum<kLanes>(sum, red);
   const float rstd = rsqrtf(sum / static_cast<float>(D) + eps);
-  if (threadIdx.x == 0 && rstd_out) rstd_out[row] = rstd;
+  if (threadIdx.x == 0 && cols && rstd_out) rstd_out[row] = rstd;
   uint32_t amax = 0;
 #pragma unroll
   for (int i = 0; i < V; ++i) {
     const int c = (threadIdx.x + i * step) * 8;
-    if (c < D) {
+    if (c < cols) {
       if (res_out) store8(res_out + base + c, s[i]);
       float wv[8];
       load8(w + c, wv);
@@ -215,47 +220,47 @@ __global__ void __launch_bounds__(512)
     }
   }
   if (y8) {
-    amax = row_max<kWarp>(amax, redm);
+    amax = row_max<kLanes>(amax, redm);
     float scale, inv;
     row_scale(amax, scale, inv);
-    if (threadIdx.x == 0) y_scale[row] = scale;
+    if (threadIdx.x == 0 && cols) y_scale[row] = scale;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       const int c = (threadIdx.x + i * step) * 8;
-      if (c < D) store_codes(y8 + base + c, s[i], inv);
+      if (c < cols) store_codes(y8 + base + c, s[i], inv);
     }
   }
 }
 
-template <typename XT, int V, bool kWarp>
+template <typename XT, int V, int kLanes>
 __global__ void __launch_bounds__(512)
     quant_rows_kernel(const XT* __restrict__ x, int64_t rows, int D,
                                   uint8_t* __restrict__ q, float* __restrict__ scale_out) {
   __shared__ uint32_t redm[32];
   const int64_t row =
-      kWarp ? blockIdx.x * static_cast<int64_t>(blockDim.y) + threadIdx.y : blockIdx.x;
-  if (kWarp && row >= rows) return;
-  const int step = kWarp ? 32 : blockDim.x;
+      kLanes ? blockIdx.x * static_cast<int64_t>(blockDim.y) + threadIdx.y : blockIdx.x;
+  const int cols = kLanes && row >= rows ? 0 : D;  // no row: no columns
+  const int step = kLanes ? kLanes : blockDim.x;
   const int64_t base = row * D;
   float s[V][8];
   uint32_t amax = 0;
 #pragma unroll
   for (int i = 0; i < V; ++i) {
     const int c = (threadIdx.x + i * step) * 8;
-    if (c < D) {
+    if (c < cols) {
       load8(x + base + c, s[i]);
 #pragma unroll
       for (int j = 0; j < 8; ++j) amax = max(amax, abs_bits(s[i][j]));
     }
   }
-  amax = row_max<kWarp>(amax, redm);
+  amax = row_max<kLanes>(amax, redm);
   float scale, inv;
   row_scale(amax, scale, inv);
-  if (threadIdx.x == 0) scale_out[row] = scale;
+  if (threadIdx.x == 0 && cols) scale_out[row] = scale;
 #pragma unroll
   for (int i = 0; i < V; ++i) {
     const int c = (threadIdx.x + i * step) * 8;
-    if (c < D) store_codes(q + base + c, s[i], inv);
+    if (c < cols) store_codes(q + base + c, s[i], inv);
   }
 }
 
@@ -268,22 +273,23 @@ __global__ void __launch_bounds__(512)
 // none ahead, the kernel took 179 us for 32768 x 2560 bf16 where the bytes take
 // 128).
 // Short rows leave room for several in a CTA, each with threads of its own
-// (blockDim.y of them; a warp each for up to 512 columns, kWarp): the CTA's sums of
+// (blockDim.y of them; 8, 16 or 32 lanes of a warp for up to
+// 64, 128 or 512 columns, kLanes): the CTA's sums of
 // dw are theirs, added in order. With one row per CTA the workspace's 512 rows
 // left SMs half empty: 11564 x 112 bf16 took 20 us (8 here), 20000 x 1024 57 (38).
 // One step per thread is held to 64 registers, for 1024 threads per SM: without
 // the bound 20000 x 1024 took 48 us and 32768 x 2560 178 (136).
-template <typename XT, typename RT, int V, bool kWarp, bool kGroups>
+template <typename XT, typename RT, int V, int kLanes, bool kGroups>
 __global__ void __launch_bounds__(512, V == 1 ? 2 : 1)
     add_rmsnorm_bwd_kernel(const XT* __restrict__ dy, const RT* dres_out,
                            const RT* __restrict__ s, int64_t T, int D,
                            const float* __restrict__ w, const float* __restrict__ rstd,
                            XT* __restrict__ dx, RT* dres, float* __restrict__ dw_part) {
   constexpr bool kAhead = V <= 2;
-  constexpr bool kSeveral = kWarp || kGroups;
+  constexpr bool kSeveral = kLanes || kGroups;
   __shared__ float red[2][kGroups ? kNormBwdGroups : 1][32];
   __shared__ float group_dw[kSeveral ? 4096 : 1];  // [blockDim.y][D]
-  const int step = kWarp ? 32 : blockDim.x;
+  const int step = kLanes ? kLanes : blockDim.x;
   const int64_t row0 = kSeveral ? int64_t(blockIdx.x) * blockDim.y + threadIdx.y : blockIdx.x;
   const int64_t row_step = kSeveral ? int64_t(gridDim.x) * blockDim.y : gridDim.x;
   float dw[V][8];
@@ -312,8 +318,11 @@ __global__ void __launch_bounds__(512, V == 1 ? 2 : 1)
   };
   if (kAhead) fetch(row0);
   int buf = 0;
-  for (int64_t row = row0; row < T; row += row_step, buf ^= 1) {
+  // a warp's rows go on together
+  const int after = kLanes ? threadIdx.y % (32 / (kLanes ? kLanes : 32)) : 0;
+  for (int64_t row = row0; row - after < T; row += row_step, buf ^= 1) {
     const int64_t base = row * D;
+    const int cols = kLanes && kLanes < 32 && row >= T ? 0 : D;
     if (!kAhead) fetch(row);
     const float rr = r;
     float g[V][8], sv[V][8];
@@ -321,7 +330,7 @@ __global__ void __launch_bounds__(512, V == 1 ? 2 : 1)
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       const int c = (threadIdx.x + i * step) * 8;
-      if (c < D) {
+      if (c < cols) {
         float wv[8];
         if constexpr (kAhead) {
           values(rg[i], g[i]);
@@ -347,12 +356,12 @@ __global__ void __launch_bounds__(512, V == 1 ? 2 : 1)
     }
     // two buffers: a warp may still read this row's sums when another one
     // writes the next row's, never two rows on
-    dot = row_sum<kWarp, kGroups>(dot, red[buf][kGroups ? threadIdx.y : 0]);
+    dot = row_sum<kLanes, kGroups>(dot, red[buf][kGroups ? threadIdx.y : 0]);
     const float k = rr * rr * (dot * inv_d);
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       const int c = (threadIdx.x + i * step) * 8;
-      if (c < D) {
+      if (c < cols) {
         float d[8];
         if (dres_out) {
           if constexpr (kAhead)
@@ -414,21 +423,26 @@ __global__ void __launch_bounds__(1024)
   }
 }
 
-// Steps per thread (V) and the launch of one row's threads for D columns:
-// rows of up to 512 columns take a warp, up to 4096 columns one step of a CTA
-// with a thread for each 8 columns, longer ones more steps.
+// Steps per thread (V), lanes of a warp (or 0) and the launch of one row's
+// threads for D columns: rows of up to 64, 128 or 512 columns take a quarter, half
+// or all of a warp, up to 4096 columns one step of a CTA with a thread for each 8
+// columns, longer ones more steps. (With a warp for each row of 64 bf16 columns
+// 262144 of them took 57 us, their gradient 73; 21 and 32 with a quarter.)
 struct RowShape {
   int V;
-  bool warp;
+  int lanes;
   dim3 block;
 };
 RowShape row_shape(int D) {
   const int nvec = D / 8;
-  if (nvec <= 64) return {nvec <= 32 ? 1 : 2, true, dim3(32, 8, 1)};
+  if (nvec <= 64) {
+    const int lanes = nvec <= 8 ? 8 : nvec <= 16 ? 16 : 32;
+    return {nvec <= 32 ? 1 : 2, lanes, dim3(lanes, 256 / lanes, 1)};
+  }
   int V = 1;
   while (nvec > V * 512 && V < 4) V *= 2;
   const int threads = ((nvec + V - 1) / V + 31) / 32 * 32;
-  return {V, false, dim3(static_cast<unsigned>(threads), 1, 1)};
+  return {V, 0, dim3(static_cast<unsigned>(threads), 1, 1)};
 }
 
 template <typename XT, typename RT>
@@ -436,23 +450,25 @@ cudaError_t add_rmsnorm(const void* x, const void* res, int64_t T, int D, const 
                         float eps, void* res_out, void* y, void* y8, float* y_scale, float* rstd,
                         cudaStream_t stream) {
   const RowShape sh = row_shape(D);
-  const unsigned grid = static_cast<unsigned>(sh.warp ? (T + 7) / 8 : T);
+  const unsigned grid = static_cast<unsigned>(sh.lanes ? (T + sh.block.y - 1) / sh.block.y : T);
   auto go = [&](auto kern) {
     kern<<<grid, sh.block, 0, stream>>>(
         static_cast<const XT*>(x), static_cast<const RT*>(res), T, D, w, eps,
         static_cast<RT*>(res_out), static_cast<XT*>(y), static_cast<uint8_t*>(y8), y_scale, rstd);
     return cudaGetLastError();
   };
-  if (sh.warp)
-    return sh.V == 1 ? go(add_rmsnorm_kernel<XT, RT, 1, true>)
-                     : go(add_rmsnorm_kernel<XT, RT, 2, true>);
+  if (sh.lanes)
+    return sh.lanes == 8    ? go(add_rmsnorm_kernel<XT, RT, 1, 8>)
+           : sh.lanes == 16 ? go(add_rmsnorm_kernel<XT, RT, 1, 16>)
+           : sh.V == 1      ? go(add_rmsnorm_kernel<XT, RT, 1, 32>)
+                            : go(add_rmsnorm_kernel<XT, RT, 2, 32>);
   switch (sh.V) {
     case 1:
-      return go(add_rmsnorm_kernel<XT, RT, 1, false>);
+      return go(add_rmsnorm_kernel<XT, RT, 1, 0>);
     case 2:
-      return go(add_rmsnorm_kernel<XT, RT, 2, false>);
+      return go(add_rmsnorm_kernel<XT, RT, 2, 0>);
     default:
-      return go(add_rmsnorm_kernel<XT, RT, 4, false>);
+      return go(add_rmsnorm_kernel<XT, RT, 4, 0>);
   }
 }
 
@@ -460,21 +476,24 @@ template <typename XT>
 cudaError_t quant_rows(const void* x, int64_t rows, int D, void* q, float* scale,
                        cudaStream_t stream) {
   const RowShape sh = row_shape(D);
-  const unsigned grid = static_cast<unsigned>(sh.warp ? (rows + 7) / 8 : rows);
+  const unsigned grid = static_cast<unsigned>(sh.lanes ? (rows + sh.block.y - 1) / sh.block.y : rows);
   auto go = [&](auto kern) {
     kern<<<grid, sh.block, 0, stream>>>(static_cast<const XT*>(x), rows, D,
                                         static_cast<uint8_t*>(q), scale);
     return cudaGetLastError();
   };
-  if (sh.warp)
-    return sh.V == 1 ? go(quant_rows_kernel<XT, 1, true>) : go(quant_rows_kernel<XT, 2, true>);
+  if (sh.lanes)
+    return sh.lanes == 8    ? go(quant_rows_kernel<XT, 1, 8>)
+           : sh.lanes == 16 ? go(quant_rows_kernel<XT, 1, 16>)
+           : sh.V == 1      ? go(quant_rows_kernel<XT, 1, 32>)
+                            : go(quant_rows_kernel<XT, 2, 32>);
   switch (sh.V) {
     case 1:
-      return go(quant_rows_kernel<XT, 1, false>);
+      return go(quant_rows_kernel<XT, 1, 0>);
     case 2:
-      return go(quant_rows_kernel<XT, 2, false>);
+      return go(quant_rows_kernel<XT, 2, 0>);
     default:
-      return go(quant_rows_kernel<XT, 4, false>);
+      return go(quant_rows_kernel<XT, 4, 0>);
   }
 }
 
@@ -486,7 +505,7 @@ cudaError_t add_rmsnorm_bwd(const void* dy, const void* dres_out, const void* s,
   // Two rows or more per row's threads, up to 1024 threads per SM.
   const int per_row = static_cast<int>(sh.block.x);
   const int rows_at_once =
-      sh.warp ? kNormBwdWarps : sh.V > 1 ? 1 : std::max(1, std::min(kNormBwdGroups, 512 / per_row));
+      sh.lanes ? static_cast<int>(sh.block.y) : sh.V > 1 ? 1 : std::max(1, std::min(kNormBwdGroups, 512 / per_row));
   const int threads = per_row * rows_at_once;
   const int64_t grid = std::min<int64_t>(
       {(T + 2 * rows_at_once - 1) / (2 * rows_at_once), kNormBwdMaxParts,
@@ -499,15 +518,17 @@ cudaError_t add_rmsnorm_bwd(const void* dy, const void* dres_out, const void* s,
     return cudaGetLastError();
   };
   cudaError_t err;
-  if (sh.warp)
-    err = sh.V == 1 ? go(add_rmsnorm_bwd_kernel<XT, RT, 1, true, false>)
-                    : go(add_rmsnorm_bwd_kernel<XT, RT, 2, true, false>);
+  if (sh.lanes)
+    err = sh.lanes == 8    ? go(add_rmsnorm_bwd_kernel<XT, RT, 1, 8, false>)
+          : sh.lanes == 16 ? go(add_rmsnorm_bwd_kernel<XT, RT, 1, 16, false>)
+          : sh.V == 1      ? go(add_rmsnorm_bwd_kernel<XT, RT, 1, 32, false>)
+                           : go(add_rmsnorm_bwd_kernel<XT, RT, 2, 32, false>);
   else if (rows_at_once > 1)
-    err = go(add_rmsnorm_bwd_kernel<XT, RT, 1, false, true>);
+    err = go(add_rmsnorm_bwd_kernel<XT, RT, 1, 0, true>);
   else
-    err = sh.V == 1   ? go(add_rmsnorm_bwd_kernel<XT, RT, 1, false, false>)
-          : sh.V == 2 ? go(add_rmsnorm_bwd_kernel<XT, RT, 2, false, false>)
-                      : go(add_rmsnorm_bwd_kernel<XT, RT, 4, false, false>);
+    err = sh.V == 1   ? go(add_rmsnorm_bwd_kernel<XT, RT, 1, 0, false>)
+          : sh.V == 2 ? go(add_rmsnorm_bwd_kernel<XT, RT, 2, 0, false>)
+                      : go(add_rmsnorm_bwd_kernel<XT, RT, 4, 0, false>);
   if (err != cudaSuccess || !dw) return err;
   dw_reduce_kernel<<<static_cast<unsigned>((D + 31) / 32), 1024, 0, stream>>>(
       ws, static_cast<int>(grid), D, dw);

@@ -142,10 +142,10 @@ def run_norm(x, res, w, eps, rt, q8=True):
 
 
 @gpu
-@pytest.mark.parametrize("D", [8, 64, 248, 256, 264, 512, 520, 1000, 2048, 4096, 4104, 8192, 16384])
+@pytest.mark.parametrize("D", [8, 64, 72, 128, 136, 248, 256, 264, 512, 520, 1000, 2048, 4096, 4104, 8192, 16384])
 @pytest.mark.parametrize("dtype,rt", [(BF16, F32), (BF16, BF16), (F32, F32)])
 def test_add_rmsnorm_matches_the_formula(D, dtype, rt):
-    for T in (1, 9):
+    for T in (1, 9, 67):
         x, res, w = make_rows(T, D, dtype, rt, seed=D + T)
         check_norm(x, res, w, 1e-5, run_norm(x, res, w, 1e-5, rt), f"D={D} T={T}")
 
@@ -227,7 +227,7 @@ def bwd_reference(dy, dres, s, w, rstd):
 
 @gpu
 @pytest.mark.parametrize("T,D", [(1, 8), (1, 16384), (3, 264), (37, 1000), (700, 64), (517, 1024),
-                                 (600, 4104), (64, 8200)])
+                                 (600, 4104), (64, 8200), (515, 56), (70, 72), (333, 128), (9, 136), (1203, 1536), (1001, 2048)])
 @pytest.mark.parametrize("dtype,rt", [(BF16, F32), (BF16, BF16), (F32, F32)])
 def test_add_rmsnorm_bwd_matches_the_formula(T, D, dtype, rt):
     dy, dres, w = make_rows(T, D, dtype, rt, seed=T + D)
@@ -315,7 +315,7 @@ def test_add_rmsnorm_repeats_bit_for_bit_and_empty_batches():
 
 @gpu
 @pytest.mark.parametrize("dtype", [BF16, F32])
-@pytest.mark.parametrize("rows,K", [(1, 8), (77, 264), (9, 1000), (5, 4096), (3, 16384)])
+@pytest.mark.parametrize("rows,K", [(1, 8), (69, 64), (131, 104), (77, 264), (9, 1000), (5, 4096), (3, 16384)])
 def test_quant_rows_gives_the_definitions_codes(rows, K, dtype):
     g = torch.Generator().manual_seed(K)
     x = (torch.randn(rows, K, generator=g) * 10.0 ** torch.randint(-20, 20, (rows, 1), generator=g)).to(dtype)
