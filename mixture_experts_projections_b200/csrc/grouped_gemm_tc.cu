@@ -134,12 +134,18 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
 
 // Epilogue of one accumulator tile for one warp: thread i reads TMEM lane
 // t_row.lane + i, i.e. sorted row `prow` (stored only when `valid`), the
-// 32-column chunks c0 .. c1 - 1 of output columns n0 .. n0 + w - 1 (w = 128 for the gate modes, whose z columns
-// follow the w u columns in TMEM, 256 otherwise; half of that for the half
-// tiles of a last wave). The
-// float32 outputs (per-slot partials) go row by row through the warp's
-// staging tile `stg` (row-coalesced stores); the bf16 rows, half as wide,
-// are stored directly in 16-byte pieces, which measured faster for them.
+// 32-column chunks c0 .. c1 - 1 of output columns n0 .. n0 + w - 1 (w = 128 for
+// the gate modes, whose z columns follow the w u columns in TMEM, 256 otherwise;
+// half of that for the half tiles of a last wave). The float32 outputs (per-slot
+// partials), and in 8 bits the bf16 rows too, go through the warp's staging tile
+// `stg`, so that a store instruction writes consecutive bytes of a few rows; the
+// bf16 rows of bf16 products, half as wide and half as frequent, are stored
+// directly in 16-byte pieces, which measured faster for them. `own` and, for the
+// columns' scales, 512 bytes at `sws` are the 8-bit epilogue's: it is handed the
+// tile's slots, weights and scales, which the caller read during the tile before
+// (9272 rows of K 464 and N 2944 over 16 experts: 38.6 us with these loads, the
+// rows' addresses and an arrival that waited for the stores in each chunk's way,
+// 27.2 so).
 // What a tile's row needs besides its accumulator: its slot, routing weight (or
 // 1) and scale, and of a lane the scales of up to 128 columns (four of its own:
 // of the chunks' columns, and of W_g's behind W_in's for the gate modes).
@@ -184,7 +190,8 @@ __device__ __forceinline__ void epilogue_rows(const Params& p, uint32_t t_row, b
     const int mine = valid ? static_cast<int>(row) : -1, lane = threadIdx.x & 31;
 #pragma unroll
     for (int i = 0; i < 8; ++i)
-      rows[i] = __shfl_sync(0xffffffffu, mine, kF32 ? 4 * i + (lane >> 3) : (8 * i + (lane >> 2)) & 31);
+      rows[i] = __shfl_sync(0xffffffffu, mine,
+                            kF32 ? 4 * i + (lane >> 3) : (8 * i + (lane >> 2)) & 31);
   }
   if (kQ8) {  // the columns' scales, 32 of a chunk in a row
 #pragma unroll
@@ -341,8 +348,8 @@ constexpr size_t kPairCtlBytes = (sizeof(PairCtl) + 15) / 16 * 16;
 template <int MODE, bool kQ8>
 constexpr size_t pair_smem_bytes() {
   using Geo = PairGeo<MODE, kQ8>;
-  return Geo::kStages * P_STAGE_BYTES + kPairCtlBytes + Geo::kEpiWarps * (Geo::kStageTile + Geo::kScales) +
-         1024;
+  return Geo::kStages * P_STAGE_BYTES + kPairCtlBytes +
+         Geo::kEpiWarps * (Geo::kStageTile + Geo::kScales) + 1024;
 }
 
 template <int MODE, bool kQ8>

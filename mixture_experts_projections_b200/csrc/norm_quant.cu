@@ -476,7 +476,8 @@ template <typename XT>
 cudaError_t quant_rows(const void* x, int64_t rows, int D, void* q, float* scale,
                        cudaStream_t stream) {
   const RowShape sh = row_shape(D);
-  const unsigned grid = static_cast<unsigned>(sh.lanes ? (rows + sh.block.y - 1) / sh.block.y : rows);
+  const unsigned grid =
+      static_cast<unsigned>(sh.lanes ? (rows + sh.block.y - 1) / sh.block.y : rows);
   auto go = [&](auto kern) {
     kern<<<grid, sh.block, 0, stream>>>(static_cast<const XT*>(x), rows, D,
                                         static_cast<uint8_t*>(q), scale);
@@ -505,7 +506,9 @@ cudaError_t add_rmsnorm_bwd(const void* dy, const void* dres_out, const void* s,
   // Two rows or more per row's threads, up to 1024 threads per SM.
   const int per_row = static_cast<int>(sh.block.x);
   const int rows_at_once =
-      sh.lanes ? static_cast<int>(sh.block.y) : sh.V > 1 ? 1 : std::max(1, std::min(kNormBwdGroups, 512 / per_row));
+      sh.lanes   ? static_cast<int>(sh.block.y)
+      : sh.V > 1 ? 1
+                 : std::max(1, std::min(kNormBwdGroups, 512 / per_row));
   const int threads = per_row * rows_at_once;
   const int64_t grid = std::min<int64_t>(
       {(T + 2 * rows_at_once - 1) / (2 * rows_at_once), kNormBwdMaxParts,
