@@ -993,10 +993,10 @@ def block_forward_w4(x, w_r, bias, w_conv, w_gate, w_out, k, renorm=False, bufs=
 class ResidualBlock:
     """One pre-norm block: ``norm`` (NormBuffers) and ``block`` (the block's
     buffers); ``out`` is the block's output, ``residual`` the residual stream
-    that the next block's norm adds it to."""
+    that the next block's norm adds it to. ``renorm``: as the block ran."""
 
-    def __init__(self, norm, block):
-        self.norm, self.block = norm, block
+    def __init__(self, norm, block, renorm):
+        self.norm, self.block, self.renorm = norm, block, renorm
         self.out, self.residual = block.out, norm.residual
 
 
@@ -1019,18 +1019,25 @@ def residual_block_forward(x, residual, norm_w, w_r, bias, w_conv, w_gate, w_out
     else:
         with _scope(x, stream):
             block = block_forward(*args, bufs=bufs, stream=stream, keep_uz=keep_uz)
-    return ResidualBlock(norm, block)
+    return ResidualBlock(norm, block, renorm)
 
 
-def residual_block_backward(fwd, dout, norm_w, w_r, w_conv, w_gate, w_out, renorm=True, bias=None,
+def residual_block_backward(fwd, dout, norm_w, w_r, w_conv, w_gate, w_out, renorm=None, bias=None,
                             dresidual=None, bufs=None, norm_bufs=None, stream=None,
                             grad_sync=None):
     """Backward of residual_block_forward on bf16 weights: dout [T, Dm] is the
     gradient of the block's output, ``dresidual`` that of the residual stream
     from the layers after it (or None). Returns (BackwardBuffers, NormGrads):
     the expert and router gradients, and dx / dresidual of the block's inputs
-    with the norm weight's dw. With ``grad_sync`` the norm weight's gradient is
-    summed over the ranks too."""
+    with the norm weight's dw. ``renorm``: None (as the forward ran) or that same
+    value. With ``grad_sync`` the norm weight's gradient is summed over the ranks
+    too."""
+    if not isinstance(fwd.block, BlockBuffers):
+        raise RomError("the blocks on 8-bit and 4-bit weights have no backward")
+    if renorm is None:
+        renorm = fwd.renorm
+    elif bool(renorm) != bool(fwd.renorm):
+        raise RomError(f"the forward ran with renorm={fwd.renorm}")
     with _scope(dout, stream):
         bwd = block_backward(fwd.block, dout, w_r, w_conv, w_gate, w_out, renorm, bufs, stream,
                              x=fwd.norm.y, bias=bias, grad_sync=grad_sync)

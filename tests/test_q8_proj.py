@@ -352,3 +352,34 @@ def test_norm_and_block_train_together():
     assert ((g.dx.cpu().double() - ds).abs() <= err * (1 + h) + h * ds.abs()).all()
     assert ((g.dresidual.cpu().double() - ds).abs() <= err + U * ds.abs()).all()
     assert ((g.dw.cpu().double() - dw).abs() <= dw_err).all()
+
+
+def test_residual_block_backward_refuses_other_blocks_and_weights_modes():
+    class Norm:
+        residual = None
+
+    class Fake:
+        out = None
+
+    plain = rom.BlockBuffers.__new__(rom.BlockBuffers)
+    plain.out = None
+    with pytest.raises(rom.RomError, match="no backward"):
+        rom.residual_block_backward(rom.ResidualBlock(Norm(), Fake(), True), *[None] * 6)
+    for ran, asked in ((True, False), (False, True)):
+        with pytest.raises(rom.RomError, match="renorm="):
+            rom.residual_block_backward(rom.ResidualBlock(Norm(), plain, ran), *[None] * 6, renorm=asked)
+
+
+@gpu
+@pytest.mark.parametrize("renorm", [True, False])
+def test_residual_block_backward_takes_the_forwards_weights_mode(renorm):
+    T, Dm, De, E = 70, 256, 256, 4  # (the backward takes multiples of 256)
+    inp = make_block_inputs(T, Dm, De, E, seed=6, with_dout=True)
+    d = block_to_dev(inp, "bf16")
+    nw = torch.ones(Dm, device="cuda")
+    dout = torch.from_numpy(inp["dout"]).to(BF16).cuda()
+    ws = (d["w_conv"], d["w_gate"], d["w_out"])
+    f = rom.residual_block_forward(d["x"], None, nw, d["w_r"], None, *ws, 2, renorm)
+    bwd, _ = rom.residual_block_backward(f, dout, nw, d["w_r"], *ws)
+    ref = rom.block_backward(f.block, dout, d["w_r"], *ws, renorm=renorm, x=f.norm.y)
+    assert torch.equal(ref.dx, bwd.dx) and torch.equal(ref.dlogits, bwd.dlogits)
