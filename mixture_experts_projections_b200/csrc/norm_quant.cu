@@ -184,6 +184,7 @@ __global__ void __launch_bounds__(512)
   const int64_t base = row * D;
   float s[V][8];
   float sum = 0.f;
+  pdl_wait();
 #pragma unroll
   for (int i = 0; i < V; ++i) {
     const int c = (threadIdx.x + i * step) * 8;
@@ -246,6 +247,7 @@ __global__ void __launch_bounds__(512)
   const int64_t base = row * D;
   float s[V][8];
   uint32_t amax = 0;
+  pdl_wait();
 #pragma unroll
   for (int i = 0; i < V; ++i) {
     const int c = (threadIdx.x + i * step) * 8;
@@ -317,6 +319,7 @@ __global__ void __launch_bounds__(512, V == 1 ? 2 : 1)
       }
     }
   };
+  pdl_wait();
   if (kAhead) fetch(row0);
   int buf = 0;
   // a warp's rows go on together
@@ -380,6 +383,7 @@ __global__ void __launch_bounds__(512, V == 1 ? 2 : 1)
       }
     }
   }
+  pdl_launch_dependents();  // the sum of the CTAs' dw may be set up
   if (kSeveral) {
     if (!dw_part) return;
 #pragma unroll
@@ -410,6 +414,7 @@ __global__ void __launch_bounds__(1024)
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int c = blockIdx.x * 32 + lane;
   float v = 0.f;
+  pdl_wait();  // the workspace is complete from here
   if (c < D) {
 #pragma unroll 4
     for (int p = warp; p < P; p += 32) v += part[static_cast<int64_t>(p) * D + c];
@@ -422,6 +427,23 @@ __global__ void __launch_bounds__(1024)
     for (int i = 1; i < 32; ++i) t += sum[i][lane];
     dw[c] = t;
   }
+}
+
+// Launches that may be set up while the kernel before on the stream finishes
+// (every kernel here waits for it first): 517 x 1024 bf16 rows' gradient, 8.2 us
+// with plain launches of its two kernels, 7.5 with the second one so.
+template <typename... P, typename... A>
+cudaError_t launch(void (*kern)(P...), int64_t grid, dim3 block, cudaStream_t stream, A... args) {
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(grid), 1, 1);
+  cfg.blockDim = block;
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, static_cast<P>(args)...);
 }
 
 // Steps per thread (V), lanes of a warp (or 0) and the launch of one row's
@@ -453,10 +475,9 @@ cudaError_t add_rmsnorm(const void* x, const void* res, int64_t T, int D, const 
   const RowShape sh = row_shape(D);
   const unsigned grid = static_cast<unsigned>(sh.lanes ? (T + sh.block.y - 1) / sh.block.y : T);
   auto go = [&](auto kern) {
-    kern<<<grid, sh.block, 0, stream>>>(
-        static_cast<const XT*>(x), static_cast<const RT*>(res), T, D, w, eps,
-        static_cast<RT*>(res_out), static_cast<XT*>(y), static_cast<uint8_t*>(y8), y_scale, rstd);
-    return cudaGetLastError();
+    return launch(kern, grid, sh.block, stream, static_cast<const XT*>(x),
+                  static_cast<const RT*>(res), T, D, w, eps, static_cast<RT*>(res_out),
+                  static_cast<XT*>(y), static_cast<uint8_t*>(y8), y_scale, rstd);
   };
   if (sh.lanes)
     return sh.lanes == 8    ? go(add_rmsnorm_kernel<XT, RT, 1, 8>)
@@ -480,9 +501,8 @@ cudaError_t quant_rows(const void* x, int64_t rows, int D, void* q, float* scale
   const unsigned grid =
       static_cast<unsigned>(sh.lanes ? (rows + sh.block.y - 1) / sh.block.y : rows);
   auto go = [&](auto kern) {
-    kern<<<grid, sh.block, 0, stream>>>(static_cast<const XT*>(x), rows, D,
-                                        static_cast<uint8_t*>(q), scale);
-    return cudaGetLastError();
+    return launch(kern, grid, sh.block, stream, static_cast<const XT*>(x), rows, D,
+                  static_cast<uint8_t*>(q), scale);
   };
   if (sh.lanes)
     return sh.lanes == 8    ? go(quant_rows_kernel<XT, 1, 8>)
@@ -516,10 +536,9 @@ cudaError_t add_rmsnorm_bwd(const void* dy, const void* dres_out, const void* s,
        static_cast<int64_t>(device_sm_count()) * std::max(1, 1024 / threads)});
   const dim3 block(per_row, rows_at_once, 1);
   auto go = [&](auto kern) {
-    kern<<<static_cast<unsigned>(grid), block, 0, stream>>>(
-        static_cast<const XT*>(dy), static_cast<const RT*>(dres_out), static_cast<const RT*>(s), T,
-        D, w, rstd, static_cast<XT*>(dx), static_cast<RT*>(dres), dw ? ws : nullptr);
-    return cudaGetLastError();
+    return launch(kern, grid, block, stream, static_cast<const XT*>(dy),
+                  static_cast<const RT*>(dres_out), static_cast<const RT*>(s), T, D, w, rstd,
+                  static_cast<XT*>(dx), static_cast<RT*>(dres), dw ? ws : nullptr);
   };
   cudaError_t err;
   if (sh.lanes)
@@ -534,9 +553,8 @@ cudaError_t add_rmsnorm_bwd(const void* dy, const void* dres_out, const void* s,
           : sh.V == 2 ? go(add_rmsnorm_bwd_kernel<XT, RT, 2, 0, false>)
                       : go(add_rmsnorm_bwd_kernel<XT, RT, 4, 0, false>);
   if (err != cudaSuccess || !dw) return err;
-  dw_reduce_kernel<<<static_cast<unsigned>((D + 31) / 32), 1024, 0, stream>>>(
-      ws, static_cast<int>(grid), D, dw);
-  return cudaGetLastError();
+  return launch(dw_reduce_kernel, (D + 31) / 32, dim3(1024), stream, ws, static_cast<int>(grid), D,
+                dw);
 }
 
 }  // namespace
