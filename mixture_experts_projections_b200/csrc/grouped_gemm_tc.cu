@@ -375,6 +375,26 @@ __global__ void __launch_bounds__(PairGeo<MODE, kQ8>::kThreads, 1)
   const int pair = static_cast<int>(blockIdx.x >> 1);
   const int npairs = static_cast<int>(gridDim.x >> 1);
 
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < P_STAGES; ++s) {
+      mbar_init(&ctl.full[s], 1);
+      mbar_init(&ctl.empty[s], 1);
+    }
+    for (int a = 0; a < 2; ++a) {
+      mbar_init(&ctl.tfull[a], 1);
+      mbar_init(&ctl.tempty[a], 2 * kEpiWarps);
+    }
+    mbar_init(&ctl.drain, 1);
+    ctl.abort = 0;
+    fence_barrier_init();
+    tma_prefetch_desc(&tmA);
+    tma_prefetch_desc(kGate && !leader ? &tmB1 : &tmB0);
+  }
+  if (warp == 1) {
+    tmem_alloc_pair(&ctl.tmem_base, TMEM_COLS);
+    tmem_relinquish_pair();
+  }
+  if (kQ8) pdl_wait();  // the sorted rows and their routing are complete from here
   for (int i = threadIdx.x; i <= E; i += PairGeo<MODE, kQ8>::kThreads)
     ctl.off[i] = offset_of(p, i);
   __syncthreads();
@@ -387,25 +407,6 @@ __global__ void __launch_bounds__(PairGeo<MODE, kQ8>::kThreads, 1)
       run += mt * p.n_tiles_n;
     }
     ctl.tile_start[E] = run;
-    for (int s = 0; s < P_STAGES; ++s) {
-      mbar_init(&ctl.full[s], 1);
-      mbar_init(&ctl.empty[s], 1);
-    }
-    for (int a = 0; a < 2; ++a) {
-      mbar_init(&ctl.tfull[a], 1);
-      mbar_init(&ctl.tempty[a], 2 * kEpiWarps);
-    }
-    mbar_init(&ctl.drain, 1);
-    ctl.abort = 0;
-    fence_barrier_init();
-  }
-  if (warp == 0 && lane == 0) {
-    tma_prefetch_desc(&tmA);
-    tma_prefetch_desc(kGate && !leader ? &tmB1 : &tmB0);
-  }
-  if (warp == 1) {
-    tmem_alloc_pair(&ctl.tmem_base, TMEM_COLS);
-    tmem_relinquish_pair();
   }
   tc_fence_before();
   cluster_sync_all();  // barriers initialised in both CTAs before any remote use
@@ -1002,17 +1003,21 @@ cudaError_t launch_pair_mode(const CUtensorMap& a, const CUtensorMap& b0, const 
   cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          static_cast<int>(kPairSmemBytes));
   if (err != cudaSuccess) return err;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = 2;
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
+  // 8-bit products: the set-up runs while the kernel before finishes (1537 tokens,
+  // top-2, K 2048, N 1024 over 16 experts and the sum of the slots: 23.3 -> 21.2 us)
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
   cfg.blockDim = dim3(PairGeo<MODE, kQ8>::kThreads, 1, 1);
   cfg.dynamicSmemBytes = kPairSmemBytes;
   cfg.stream = stream;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = kQ8 ? 2 : 1;
   // Co-resident pairs on this device (one CTA per SM), cached per device.
   static int pairs_cache[64] = {0};
   int dev = 0;
