@@ -280,10 +280,13 @@ __global__ void __launch_bounds__(512)
 // (blockDim.y of them; 8, 16 or 32 lanes of a warp for up to 64, 128 or 512
 // columns, kLanes): the CTA's sums of dw are theirs, added in order. With one row
 // per CTA the workspace's 512 rows left SMs half empty: 11564 x 112 bf16 took 20 us (8 here), 20000 x 1024 57 (38).
-// One step per thread is held to 64 registers, for 1024 threads per SM: without
-// the bound 20000 x 1024 took 48 us and 32768 x 2560 178 (136).
+// One step per thread of bf16 rows is held to 64 registers, for 1024 threads per
+// SM: without the bound 20000 x 1024 took 48 us and 32768 x 2560 178 (136). Float32
+// rows need more than those (32768 x 1024: 105 us, 125 with the bound), and so do a
+// warp's rows with a float32 stream (131072 x 256: 93, 98).
 template <typename XT, typename RT, int V, int kLanes, bool kGroups>
-__global__ void __launch_bounds__(512, V == 1 ? 2 : 1)
+__global__ void __launch_bounds__(
+    512, V == 1 && sizeof(XT) == 2 && !(kLanes && sizeof(RT) == 4) ? 2 : 1)
     add_rmsnorm_bwd_kernel(const XT* __restrict__ dy, const RT* dres_out,
                            const RT* __restrict__ s, int64_t T, int D,
                            const float* __restrict__ w, const float* __restrict__ rstd,
