@@ -97,6 +97,17 @@ __device__ __forceinline__ void store8(__nv_bfloat16* p, const float (&v)[8]) {
   }
   *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
 }
+__device__ __forceinline__ void cp_async16(void* dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src)
+               : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() {
+  asm volatile("cp.async.commit_group;" ::: "memory");
+}
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {  // all but the last N groups
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
 // The value that storing v in T leaves.
 __device__ __forceinline__ float as_stored(float v, const float*) { return v; }
 __device__ __forceinline__ float as_stored(float v, const __nv_bfloat16*) {
@@ -274,12 +285,15 @@ __global__ void __launch_bounds__(512)
 // atomics, the same result every time. Every input of the next row is on its way
 // while the current row is summed, for up to two steps per thread, which have the
 // registers for it (with its loads after the sum's barrier, and none ahead, the
-// kernel took 179 us for 32768 x 2560 bf16 where the bytes take 128; rows of more
-// than 8192 columns still go so, at half of the copy rate).
+// kernel took 179 us for 32768 x 2560 bf16 where the bytes take 128). Longer rows
+// of a bf16 stream wait in shared memory, each thread's own pieces (5000 x 16384:
+// 136 us, 237 without; 125 by the bytes). Those of a float32 stream do not: all three
+// inputs there leave the weights no L1 (319 us, 281 without; 200 by the bytes).
 // Short rows leave room for several in a CTA, each with threads of its own
 // (blockDim.y of them; 8, 16 or 32 lanes of a warp for up to 64, 128 or 512
 // columns, kLanes): the CTA's sums of dw are theirs, added in order. With one row
-// per CTA the workspace's 512 rows left SMs half empty: 11564 x 112 bf16 took 20 us (8 here), 20000 x 1024 57 (38).
+// per CTA the workspace's 512 rows left SMs half empty: 11564 x 112 bf16 took 20 us
+// (7 here), 20000 x 1024 57 (37).
 // One step per thread of bf16 rows is held to 64 registers, for 1024 threads per
 // SM: without the bound 20000 x 1024 took 48 us and 32768 x 2560 178 (136). Float32
 // rows need more than those (32768 x 1024: 105 us, 125 with the bound), and so do a
@@ -291,7 +305,8 @@ __global__ void __launch_bounds__(
                            const RT* __restrict__ s, int64_t T, int D,
                            const float* __restrict__ w, const float* __restrict__ rstd,
                            XT* __restrict__ dx, RT* dres, float* __restrict__ dw_part) {
-  constexpr bool kAhead = V <= 2;
+  constexpr bool kAhead = V <= 2;                       // the next row in registers
+  constexpr bool kStaged = !kAhead && sizeof(RT) == 2;  // or in shared memory
   constexpr bool kSeveral = kLanes || kGroups;
   __shared__ float red[2][kGroups ? kNormBwdGroups : 1][32];
   __shared__ float group_dw[kSeveral ? 4096 : 1];  // [blockDim.y][D]
@@ -322,15 +337,43 @@ __global__ void __launch_bounds__(
       }
     }
   };
+  // A thread's pieces of the next row's dy, s and dres_out: [3 V][blockDim.x].
+  extern __shared__ uint4 staged[];
+  auto piece = [&](int i) { return staged + i * blockDim.x + threadIdx.x; };
+  auto copy = [&](int first, const auto* p, int64_t row) {
+    if (row < T && p) {
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        const int c = (threadIdx.x + i * step) * 8;
+        if (c < D) cp_async16(piece(first + i), p + row * D + c);
+      }
+    }
+  };
+  auto copy_rows = [&](int64_t row) {
+    if (row < T) r = rstd[row];
+    copy(0, dy, row);
+    copy(V, s, row);
+    cp_async_commit();
+  };
+  auto copy_dres = [&](int64_t row) {
+    copy(2 * V, dres_out, row);
+    cp_async_commit();
+  };
   pdl_wait();
-  if (kAhead) fetch(row0);
+  if constexpr (kAhead) {
+    fetch(row0);
+  } else if constexpr (kStaged) {
+    copy_rows(row0);
+    copy_dres(row0);
+  }
   int buf = 0;
   // a warp's rows go on together
   const int after = kLanes ? threadIdx.y % (32 / (kLanes ? kLanes : 32)) : 0;
   for (int64_t row = row0; row - after < T; row += row_step, buf ^= 1) {
     const int64_t base = row * D;
     const int cols = kLanes && kLanes < 32 && row >= T ? 0 : D;
-    if (!kAhead) fetch(row);
+    if constexpr (kStaged) cp_async_wait<1>();
+    if constexpr (!kAhead && !kStaged) fetch(row);
     const float rr = r;
     float g[V][8], sv[V][8];
     float dot = 0.f;
@@ -342,6 +385,9 @@ __global__ void __launch_bounds__(
         if constexpr (kAhead) {
           values(rg[i], g[i]);
           values(rs[i], sv[i]);
+        } else if constexpr (kStaged) {
+          load8(reinterpret_cast<const XT*>(piece(i)), g[i]);
+          load8(reinterpret_cast<const RT*>(piece(V + i)), sv[i]);
         } else {
           load8(dy + base + c, g[i]);
           load8(s + base + c, sv[i]);
@@ -360,11 +406,14 @@ __global__ void __launch_bounds__(
 #pragma unroll
       for (int i = 0; i < V; ++i) cd[i] = rd[i];
       fetch(row + row_step);
+    } else if constexpr (kStaged) {
+      copy_rows(row + row_step);
     }
     // two buffers: a warp may still read this row's sums when another one
     // writes the next row's, never two rows on
     dot = row_sum<kLanes, kGroups>(dot, red[buf][kGroups ? threadIdx.y : 0]);
     const float k = rr * rr * (dot * inv_d);
+    if constexpr (kStaged) cp_async_wait<1>();
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       const int c = (threadIdx.x + i * step) * 8;
@@ -373,6 +422,8 @@ __global__ void __launch_bounds__(
         if (dres_out) {
           if constexpr (kAhead)
             values(cd[i], d);
+          else if constexpr (kStaged)
+            load8(reinterpret_cast<const RT*>(piece(2 * V + i)), d);
           else
             load8(dres_out + base + c, d);
         } else {
@@ -385,6 +436,7 @@ __global__ void __launch_bounds__(
         if (dres) store8(dres + base + c, d);
       }
     }
+    if constexpr (kStaged) copy_dres(row + row_step);
   }
   pdl_launch_dependents();  // the sum of the CTAs' dw may be set up
   if (kSeveral) {
@@ -436,13 +488,15 @@ __global__ void __launch_bounds__(1024)
 // (every kernel here waits for it first): 517 x 1024 bf16 rows' gradient, 8.2 us
 // with plain launches of its two kernels, 7.5 with the second one so.
 template <typename... P, typename... A>
-cudaError_t launch(void (*kern)(P...), int64_t grid, dim3 block, cudaStream_t stream, A... args) {
+cudaError_t launch(void (*kern)(P...), int64_t grid, dim3 block, size_t smem, cudaStream_t stream,
+                   A... args) {
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(grid), 1, 1);
   cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
@@ -478,7 +532,7 @@ cudaError_t add_rmsnorm(const void* x, const void* res, int64_t T, int D, const 
   const RowShape sh = row_shape(D);
   const unsigned grid = static_cast<unsigned>(sh.lanes ? (T + sh.block.y - 1) / sh.block.y : T);
   auto go = [&](auto kern) {
-    return launch(kern, grid, sh.block, stream, static_cast<const XT*>(x),
+    return launch(kern, grid, sh.block, 0, stream, static_cast<const XT*>(x),
                   static_cast<const RT*>(res), T, D, w, eps, static_cast<RT*>(res_out),
                   static_cast<XT*>(y), static_cast<uint8_t*>(y8), y_scale, rstd);
   };
@@ -504,7 +558,7 @@ cudaError_t quant_rows(const void* x, int64_t rows, int D, void* q, float* scale
   const unsigned grid =
       static_cast<unsigned>(sh.lanes ? (rows + sh.block.y - 1) / sh.block.y : rows);
   auto go = [&](auto kern) {
-    return launch(kern, grid, sh.block, stream, static_cast<const XT*>(x), rows, D,
+    return launch(kern, grid, sh.block, 0, stream, static_cast<const XT*>(x), rows, D,
                   static_cast<uint8_t*>(q), scale);
   };
   if (sh.lanes)
@@ -536,12 +590,20 @@ cudaError_t add_rmsnorm_bwd(const void* dy, const void* dres_out, const void* s,
   // to a CTA; of warp-sized rows they cost more parts of dw than they save).
   while (!sh.lanes && rows_at_once > 1 && T < rows_at_once * device_sm_count()) rows_at_once /= 2;
   const int threads = per_row * rows_at_once;
-  const int64_t grid = std::min<int64_t>(
-      {(T + 2 * rows_at_once - 1) / (2 * rows_at_once), kNormBwdMaxParts,
-       static_cast<int64_t>(device_sm_count()) * std::max(1, 1024 / threads)});
+  const bool staged = sh.V > 2 && sizeof(RT) == 2;  // (one CTA of an SM's shared memory)
+  const int per_sm = staged ? 1 : std::max(1, 1024 / threads);
+  const int64_t grid =
+      std::min<int64_t>({(T + 2 * rows_at_once - 1) / (2 * rows_at_once), kNormBwdMaxParts,
+                         static_cast<int64_t>(device_sm_count()) * per_sm});
   const dim3 block(per_row, rows_at_once, 1);
+  const size_t smem = staged ? sizeof(uint4) * 3 * sh.V * threads : 0;
   auto go = [&](auto kern) {
-    return launch(kern, grid, block, stream, static_cast<const XT*>(dy),
+    if (smem) {
+      const cudaError_t e = cudaFuncSetAttribute(
+          kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+      if (e != cudaSuccess) return e;
+    }
+    return launch(kern, grid, block, smem, stream, static_cast<const XT*>(dy),
                   static_cast<const RT*>(dres_out), static_cast<const RT*>(s), T, D, w, rstd,
                   static_cast<XT*>(dx), static_cast<RT*>(dres), dw ? ws : nullptr);
   };
@@ -558,8 +620,8 @@ cudaError_t add_rmsnorm_bwd(const void* dy, const void* dres_out, const void* s,
           : sh.V == 2 ? go(add_rmsnorm_bwd_kernel<XT, RT, 2, 0, false>)
                       : go(add_rmsnorm_bwd_kernel<XT, RT, 4, 0, false>);
   if (err != cudaSuccess || !dw) return err;
-  return launch(dw_reduce_kernel, (D + 31) / 32, dim3(1024), stream, ws, static_cast<int>(grid), D,
-                dw);
+  return launch(dw_reduce_kernel, (D + 31) / 32, dim3(1024), 0, stream, ws,
+                static_cast<int>(grid), D, dw);
 }
 
 }  // namespace
