@@ -246,36 +246,54 @@ __global__ void __launch_bounds__(512)
   }
 }
 
+// Persistent CTAs; a row is on its way while the one before it is converted
+// (16384 x 4096 bf16: 36 us, 50 with a CTA per row and one step per thread; 31 by
+// the bytes).
 template <typename XT, int V, int kLanes>
 __global__ void __launch_bounds__(512)
-    quant_rows_kernel(const XT* __restrict__ x, int64_t rows, int D,
-                                  uint8_t* __restrict__ q, float* __restrict__ scale_out) {
-  __shared__ uint32_t redm[32];
-  const int64_t row =
-      kLanes ? blockIdx.x * static_cast<int64_t>(blockDim.y) + threadIdx.y : blockIdx.x;
-  const int cols = kLanes && row >= rows ? 0 : D;  // no row: no columns
+    quant_rows_kernel(const XT* __restrict__ x, int64_t rows, int D, uint8_t* __restrict__ q,
+                      float* __restrict__ scale_out) {
+  __shared__ uint32_t redm[2][32];
   const int step = kLanes ? kLanes : blockDim.x;
-  const int64_t base = row * D;
-  float s[V][8];
-  uint32_t amax = 0;
-  pdl_wait();
+  const int64_t row0 =
+      kLanes ? blockIdx.x * static_cast<int64_t>(blockDim.y) + threadIdx.y : blockIdx.x;
+  const int64_t row_step = kLanes ? gridDim.x * static_cast<int64_t>(blockDim.y) : gridDim.x;
+  Raw8<XT> next[V];
+  auto fetch = [&](int64_t row) {
 #pragma unroll
-  for (int i = 0; i < V; ++i) {
-    const int c = (threadIdx.x + i * step) * 8;
-    if (c < cols) {
-      load8(x + base + c, s[i]);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) amax = max(amax, abs_bits(s[i][j]));
+    for (int i = 0; i < V; ++i) {
+      const int c = (threadIdx.x + i * step) * 8;
+      if (row < rows && c < D) next[i] = load_raw(x + row * D + c);
     }
-  }
-  amax = row_max<kLanes>(amax, redm);
-  float scale, inv;
-  row_scale(amax, scale, inv);
-  if (threadIdx.x == 0 && cols) scale_out[row] = scale;
+  };
+  pdl_wait();
+  fetch(row0);
+  // a warp's rows go on together
+  const int after = kLanes ? threadIdx.y % (32 / (kLanes ? kLanes : 32)) : 0;
+  int buf = 0;
+  for (int64_t row = row0; row - after < rows; row += row_step, buf ^= 1) {
+    const int cols = kLanes && row >= rows ? 0 : D;  // no row: no columns
+    float s[V][8];
+    uint32_t amax = 0;
 #pragma unroll
-  for (int i = 0; i < V; ++i) {
-    const int c = (threadIdx.x + i * step) * 8;
-    if (c < cols) store_codes(q + base + c, s[i], inv);
+    for (int i = 0; i < V; ++i) {
+      const int c = (threadIdx.x + i * step) * 8;
+      if (c < cols) {
+        values(next[i], s[i]);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) amax = max(amax, abs_bits(s[i][j]));
+      }
+    }
+    fetch(row + row_step);
+    amax = row_max<kLanes>(amax, redm[buf]);
+    float scale, inv;
+    row_scale(amax, scale, inv);
+    if (threadIdx.x == 0 && cols) scale_out[row] = scale;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int c = (threadIdx.x + i * step) * 8;
+      if (c < cols) store_codes(q + row * D + c, s[i], inv);
+    }
   }
 }
 
@@ -513,13 +531,13 @@ struct RowShape {
   int lanes;
   dim3 block;
 };
-RowShape row_shape(int D) {
+RowShape row_shape(int D, int fewest_steps = 1) {
   const int nvec = D / 8;
   if (nvec <= 64) {
     const int lanes = nvec <= 8 ? 8 : nvec <= 16 ? 16 : 32;
     return {nvec <= 32 ? 1 : 2, lanes, dim3(lanes, 256 / lanes, 1)};
   }
-  int V = 1;
+  int V = fewest_steps;
   while (nvec > V * 512 && V < 4) V *= 2;
   const int threads = ((nvec + V - 1) / V + 31) / 32 * 32;
   return {V, 0, dim3(static_cast<unsigned>(threads), 1, 1)};
@@ -554,9 +572,11 @@ cudaError_t add_rmsnorm(const void* x, const void* res, int64_t T, int D, const 
 template <typename XT>
 cudaError_t quant_rows(const void* x, int64_t rows, int D, void* q, float* scale,
                        cudaStream_t stream) {
-  const RowShape sh = row_shape(D);
-  const unsigned grid =
-      static_cast<unsigned>(sh.lanes ? (rows + sh.block.y - 1) / sh.block.y : rows);
+  const RowShape sh = row_shape(D, 2);
+  const int64_t ctas = sh.lanes ? (rows + sh.block.y - 1) / sh.block.y : rows;
+  const int threads = static_cast<int>(sh.block.x * sh.block.y);
+  const int64_t grid =
+      std::min<int64_t>(ctas, static_cast<int64_t>(device_sm_count()) * std::max(1, 2048 / threads));
   auto go = [&](auto kern) {
     return launch(kern, grid, sh.block, 0, stream, static_cast<const XT*>(x), rows, D,
                   static_cast<uint8_t*>(q), scale);
