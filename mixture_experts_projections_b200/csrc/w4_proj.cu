@@ -52,10 +52,9 @@ constexpr int kW4MaxSlots = kW4MaxTokens * kMaxTopK;
 constexpr int kW4MaxStages = 6;
 constexpr int kW4MostSmem = 110 * 1024;   // of each of two CTAs on an SM
 constexpr int kW4ThirdSmem = 73 * 1024;   // of each of three
-// CTAs of `warps` consumer warps that an SM holds: their registers set it.
-__host__ __device__ constexpr int w4_resident(int nb, int warps) {
-  return nb == 1 && warps <= 7 ? 3 : 2;
-}
+// CTAs that an SM holds: their registers set it (of one token block, 7 consumer
+// warps with 96 each or 9 with 64).
+__host__ __device__ constexpr int w4_resident(int nb) { return nb == 1 ? 3 : 2; }
 
 struct W4Params {
   const __nv_bfloat16* x;
@@ -66,6 +65,7 @@ struct W4Params {
   int nt, kb;           // 16-row tiles, 128-column blocks
   int splits;           // CTAs of a cluster that share a row block's columns
   int max_active;       // upper bound of the experts in use
+  int resident;         // CTAs that an SM is to hold
   int passes;           // CTAs that share an expert's passes over its tokens
   int stages;           // of the ring
   int to_token;         // bf16 rows in token order (k == 1), else float32 slot rows
@@ -184,8 +184,13 @@ struct W4Maps {
 // tokens' rows by 16-byte copies that arrive on the stage's barrier. NB: 8-token
 // blocks held at a time; an expert with more tokens is passed over again. GS:
 // steps of 16 columns that share a scale (group / 16). Every wait is bounded.
-template <int NB, int GS>
-__global__ void __maxnreg__(96)
+//
+// kTight: 64 registers, for three CTAs of 8 or 9 consumer warps on an SM where
+// there are as many (19 tokens, top-2 of 16 experts of 2004 x 1000, Conv+Gate: 12.9
+// us; 14.7 with three of 7). Elsewhere the bound costs more than it gives (one
+// token, 8 experts of 4096 x 2048, top-2: 7.2 us, 6.7 without).
+template <int NB, int GS, bool kTight>
+__global__ void __maxnreg__(kTight ? 64 : 96)
     w4_proj_kernel(const __grid_constant__ W4Maps maps, const W4Params p) {
   extern __shared__ __align__(128) uint8_t smem[];
   constexpr int kTok = NB * 8;
@@ -422,9 +427,11 @@ __global__ void __maxnreg__(96)
   }
 }
 
-template <int NB, int GS>
+template <int NB, int GS, bool kTight = false>
 cudaError_t launch_w4(W4Params p, const W4Maps& maps, int warps, int mats, cudaStream_t stream) {
-  auto kern = w4_proj_kernel<NB, GS>;
+  if constexpr (NB == 1 && !kTight)
+    if (p.resident > 2 && warps > 7) return launch_w4<NB, GS, true>(p, maps, warps, mats, stream);
+  auto kern = w4_proj_kernel<NB, GS, kTight>;
   // Once per device: the most shared memory a launch asks for, and the largest
   // carve-out, so that several CTAs fit an SM.
   static std::atomic<uint64_t> ready{0};
@@ -441,7 +448,7 @@ cudaError_t launch_w4(W4Params p, const W4Maps& maps, int warps, int mats, cudaS
   }
   const int row_blks = (p.nt + warps - 1) / warps;
   const int stage = w4_stage_bytes<NB>(warps);
-  const int budget = (w4_resident(NB, warps) == 3 ? kW4ThirdSmem : kW4MostSmem) -
+  const int budget = (p.resident > 2 ? kW4ThirdSmem : kW4MostSmem) -
                      static_cast<int>(sizeof(W4Ctl));
   p.stages = std::min(kW4MaxStages, budget / stage);
   cudaLaunchAttribute attr[2];
@@ -577,7 +584,7 @@ cudaError_t launch_w4_proj(const void* x, int T, int K, const void* q0, const vo
   // Token blocks of 8 held at a time: enough for an expert with two standard
   // deviations more tokens than an even routing gives it (one with more is
   // passed over again, its weights then coming from L2): fewer blocks leave room
-  // for more CTAs. 19 tokens, top-2 of 16 experts: 14.9 us with 1, 18.1 with 3; 32
+  // for more CTAs. 19 tokens, top-2 of 16 experts: 13.0 us with 1, 18.1 with 3; 32
   // tokens, top-1 of 4: 29.0 with 2, 43 with 1.
   const double even = static_cast<double>(T) * k / E;
   const double most = std::min(static_cast<double>(T), even + 2.0 * std::sqrt(even));
@@ -604,7 +611,7 @@ cudaError_t launch_w4_proj(const void* x, int T, int K, const void* q0, const vo
     for (int s = 1; s <= 8 && s <= p.kb; s *= 2) {
       for (int w = kW4MaxWarps; w >= kW4MinWarps; --w) {
         const double ctas = std::ceil(((p.nt + w - 1) / w) * used * mats * s * z / sms);
-        const double resident = std::min(ctas, static_cast<double>(w4_resident(nb, w))) * w;
+        const double resident = std::min(ctas, static_cast<double>(w4_resident(nb))) * w;
         const double tiles = w * ((p.kb + s - 1) / s) * (1.0 + 11.0 / resident);
         const double cost = ctas * passes / z * (tiles + (s > 1 ? hand_over : 0.0));
         if (cost < best * 0.999) {
@@ -612,6 +619,7 @@ cudaError_t launch_w4_proj(const void* x, int T, int K, const void* q0, const vo
           warps = w;
           p.splits = s;
           p.passes = z;
+          p.resident = static_cast<int>(std::min<double>(ctas, w4_resident(nb)));
         }
       }
     }

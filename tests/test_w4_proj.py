@@ -121,6 +121,8 @@ CASES = [
     # an expert's passes shared by CTAs, with and without shared columns; fewer blocks of columns than CTAs of a cluster
     (60, 1504, 200, 1, 1, 64, None), (64, 264, 70, 2, 2, 32, None), (41, 72, 2500, 1, 1, 128, None),
     (20, 640, 20, 4, 1, 64, None),
+    # more CTAs of one token block than two per SM
+    (6, 256, 9000, 16, 2, 32, None), (7, 264, 8200, 16, 2, 64, None), (5, 136, 9100, 16, 3, 128, None),
 ]
 
 
