@@ -471,7 +471,8 @@ int rom_route_dispatch_noalloc(const void* x, int dtype, int64_t T, int Dm, cons
  *   a = max(max_c |v_c|, 2^-100),  scale = a / 448,  code = e4m3(v * (448 / a)),
  * rounded to nearest even; a row of zeros is zeros. A row that holds an
  * infinity or a NaN gets NaN codes and a NaN scale. Readers take any finite
- * codes and any scales.
+ * codes and any scales, as long as the products that they form are in float32's
+ * range.
  * ------------------------------------------------------------------------ */
 
 /*
@@ -550,9 +551,10 @@ int rom_dispatch_q8(const void* x8, const float* x_scale, int64_t T, int Dm, int
 /*
  * rom_expert_proj_q8 -- rom_expert_proj() on 8-bit rows and weights: for the
  * sorted row p of expert e
- *   value[p][n] = (sum_c a[p][c] w[e][n][c]) * a_scale[p] * w_scale[e][n],
- * products of e4m3 codes summed in float32 on the tensor cores, then the
- * epilogue of `proj` with its outputs in bf16 or float32.
+ *   value[p][n] = ((sum_c a[p][c] w[e][n][c]) * a_scale[p]) * w_scale[e][n],
+ * products of e4m3 codes summed in float32 on the tensor cores, the scales
+ * multiplied one after the other in this order (and the routing weight after
+ * them), then the epilogue of `proj` with its outputs in bf16 or float32.
  *
  *  proj      as rom_expert_proj; ROM_PROJ_SLOTS without routing arrays is a
  *            dense projection of the R rows (E == 1)

@@ -32,7 +32,7 @@
 //
 // The same kernels run the products in 8 bits (rom_expert_proj_q8, kQ8): rows
 // and weights in e4m3 with a float32 scale per row and per output feature,
-//   value[p][n] = (sum_c a8[p][c] w8[e][n][c]) * sa[p] * sw[e][n].
+//   value[p][n] = ((sum_c a8[p][c] w8[e][n][c]) * sa[p]) * sw[e][n].
 // A 128-byte row of a stage then holds 128 elements of K instead of 64 and one
 // MMA takes 32 of them instead of 16, so tiles, ring, descriptors and barriers
 // are those of bf16 and a stage of the same bytes does twice the work. The
@@ -94,18 +94,20 @@ struct Params {
   const float* w1_scale;
 };
 
-// 8-bit products: acc[j] *= sa * sw[j] for 32 columns, the scales of the
-// columns read from shared memory as 8 uniform 16-byte loads.
+// 8-bit products: acc[j] = (acc[j] * sa) * sw[j] for 32 columns, the scales of the
+// columns read from shared memory as 8 uniform 16-byte loads. One scale after the
+// other, in every kernel: their product alone may leave float32's range or its
+// normal numbers where the value does not.
 template <bool kQ8>
 __device__ __forceinline__ void apply_scales(uint32_t (&acc)[32], float sa, const float* sw) {
   if (kQ8) {
 #pragma unroll
     for (int v = 0; v < 8; ++v) {
       const float4 s = reinterpret_cast<const float4*>(sw)[v];
-      acc[4 * v + 0] = __float_as_uint(__uint_as_float(acc[4 * v + 0]) * (sa * s.x));
-      acc[4 * v + 1] = __float_as_uint(__uint_as_float(acc[4 * v + 1]) * (sa * s.y));
-      acc[4 * v + 2] = __float_as_uint(__uint_as_float(acc[4 * v + 2]) * (sa * s.z));
-      acc[4 * v + 3] = __float_as_uint(__uint_as_float(acc[4 * v + 3]) * (sa * s.w));
+      acc[4 * v + 0] = __float_as_uint(__uint_as_float(acc[4 * v + 0]) * sa * s.x);
+      acc[4 * v + 1] = __float_as_uint(__uint_as_float(acc[4 * v + 1]) * sa * s.y);
+      acc[4 * v + 2] = __float_as_uint(__uint_as_float(acc[4 * v + 2]) * sa * s.z);
+      acc[4 * v + 3] = __float_as_uint(__uint_as_float(acc[4 * v + 3]) * sa * s.w);
     }
   }
 }
@@ -669,19 +671,20 @@ template <int MODE>
 constexpr size_t kSwapSmemBytes =
     SwapGeo<MODE>::kStages * SwapGeo<MODE>::kStageBytes + sizeof(SwapCtl) + 1024;
 
-// Output row and router weight of one token of the tile, for the lane that
-// holds it (one token per lane, so the slot and weight loads of a chunk of
-// 32 tokens are issued together rather than one dependent pair per store).
+// Output row, router weight and (8 bits) row scale of one token of the tile, for
+// the lane that holds it (one token per lane, so the slot, weight and scale loads
+// of a chunk of 32 tokens are issued together rather than one dependent chain per
+// store).
 template <int MODE, bool kQ8>
 __device__ __forceinline__ void swap_token(const Params& p, int64_t prow, bool valid, int& orow,
-                                           float& r) {
+                                           float& r, float& sa) {
   orow = 0;
-  r = 0.f;
+  r = sa = 0.f;
   if (valid) {
     const int slot = MODE == kEpiGateH ? 0 : static_cast<int>(slot_of(p, prow));
     // no routing weights: r = 1
     r = !SwapGeo<MODE>::kGate && p.topk_w ? p.topk_w[slot] : 1.f;
-    if (kQ8) r *= p.a_scale[prow];
+    if (kQ8) sa = p.a_scale[prow];
     orow = MODE == kEpiGateH        ? static_cast<int>(prow)
            : MODE == kEpiScaleToken ? slot / p.k
                                     : slot;
@@ -867,7 +870,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       coords(tile, e, w_blk, t_blk);
       int nv;  // token columns of the tile that may be stored
       int orow[2];
-      float rw[2];
+      float rw[2], sa[2];
       bool keep[2] = {true, true};
       if (kDense) {
         nv = static_cast<int>(p.R < SW_BN ? p.R : SW_BN);  // all T tokens, one block
@@ -893,8 +896,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         nv = min(SW_BN, n_e - t_blk * SW_BN);  // valid token columns, >= 1
         // token info first: its loads overlap the wait for the accumulator
         const int64_t prow0 = static_cast<int64_t>(ctl.off[e]) + t_blk * SW_BN;
-        swap_token<MODE, kQ8>(p, prow0 + lane, lane < nv, orow[0], rw[0]);
-        swap_token<MODE, kQ8>(p, prow0 + 32 + lane, 32 + lane < nv, orow[1], rw[1]);
+        swap_token<MODE, kQ8>(p, prow0 + lane, lane < nv, orow[0], rw[0], sa[0]);
+        swap_token<MODE, kQ8>(p, prow0 + 32 + lane, 32 + lane < nv, orow[1], rw[1], sa[1]);
       }
       if (!mbar_wait(&ctl.tfull[acc], acc_phase, abort_flag, p.status)) break;
       tc_fence_after();
@@ -916,9 +919,9 @@ __global__ void __launch_bounds__(kThreads, 1)
               if constexpr (kGate) {
                 const int64_t i =
                     static_cast<int64_t>(__shfl_sync(0xffffffffu, orow[c], j)) * p.N + n;
-                const float sa = __shfl_sync(0xffffffffu, rw[c], j);
-                const float uv = __uint_as_float(a[j]) * (sa * sw);
-                const float zv = __uint_as_float(z[j]) * (sa * sw1);
+                const float row_scale = __shfl_sync(0xffffffffu, sa[c], j);
+                const float uv = __uint_as_float(a[j]) * row_scale * sw;
+                const float zv = __uint_as_float(z[j]) * row_scale * sw1;
                 if (MODE == kEpiGateH) {
                   static_cast<__nv_bfloat16*>(p.out)[i] = __float2bfloat16_rn(silu_gate(uv, zv));
                 } else {
@@ -928,8 +931,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 continue;
               }
               const int o = __shfl_sync(0xffffffffu, orow[c], j);
-              float v = __shfl_sync(0xffffffffu, rw[c], j) * __uint_as_float(a[j]);
-              if (kQ8) v *= sw;
+              float v = __uint_as_float(a[j]);
+              if (kQ8) v = v * __shfl_sync(0xffffffffu, sa[c], j) * sw;
+              v *= __shfl_sync(0xffffffffu, rw[c], j);
               const bool kept = __shfl_sync(0xffffffffu, keep[c] ? 1 : 0, j) != 0;
               const int64_t i = static_cast<int64_t>(o) * p.N + n;
               if (kept) {
