@@ -39,6 +39,9 @@ constexpr float kE4m3Max = 448.0f;
 // Rows of 520 to 2048 columns that a CTA of the backward goes through at a time:
 // as many as 512 threads hold, up to this many (of shorter rows, 8 warps' worth).
 constexpr int kNormBwdGroups = 4;
+// Most shared memory of a CTA of the backward that stages its rows: 3 pieces of 16
+// bytes, 4 steps, 512 threads.
+constexpr int kNormBwdStagedBytes = 16 * 3 * 4 * 512;
 constexpr float kAmaxFloor = 7.888609052210118e-31f;  // 2^-100
 
 // 8 elements as they are stored, and their values.
@@ -618,7 +621,7 @@ cudaError_t add_rmsnorm_bwd(const void* dy, const void* dres_out, const void* s,
   // to a CTA; of warp-sized rows they cost more parts of dw than they save).
   while (!sh.lanes && rows_at_once > 1 && T < rows_at_once * device_sm_count()) rows_at_once /= 2;
   const int threads = per_row * rows_at_once;
-  const bool staged = sh.V > 2 && sizeof(RT) == 2;  // (one CTA of an SM's shared memory)
+  const bool staged = sh.V > 2 && sizeof(RT) == 2;  // (its registers leave one CTA to an SM)
   const int per_sm = staged ? 1 : std::max(1, 1024 / threads);
   const int64_t grid =
       std::min<int64_t>({(T + 2 * rows_at_once - 1) / (2 * rows_at_once), kNormBwdMaxParts,
@@ -627,8 +630,10 @@ cudaError_t add_rmsnorm_bwd(const void* dy, const void* dres_out, const void* s,
   const size_t smem = staged ? sizeof(uint4) * 3 * sh.V * threads : 0;
   auto go = [&](auto kern) {
     if (smem) {
+      // the limit belongs to the function, not to the launch: the same for every
+      // width, or another thread's launch could find it too low for its own
       const cudaError_t e = cudaFuncSetAttribute(
-          kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+          kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kNormBwdStagedBytes);
       if (e != cudaSuccess) return e;
     }
     return launch(kern, grid, block, smem, stream, static_cast<const XT*>(dy),
