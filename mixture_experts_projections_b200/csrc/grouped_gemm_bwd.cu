@@ -441,7 +441,7 @@ __global__ void __launch_bounds__(Mode<MODE>::kThreads, 1)
         if (ragged(e, kb)) {
           const uint32_t par = (own_par >> stage) & 1u;
           own_par ^= 1u << stage;
-          if (!mbar_wait(&ctl.own[stage], par, abort_flag, p.status)) {
+          if (!mbar_wait_warp(&ctl.own[stage], par, abort_flag, p.status)) {
             ok = false;
             break;
           }
@@ -477,7 +477,7 @@ __global__ void __launch_bounds__(Mode<MODE>::kThreads, 1)
     for (int tile = pair; tile < total; tile += npairs) {
       int e, m_blk, n_blk;
       tile_of(tile, e, m_blk, n_blk);
-      if (!mbar_wait(&ctl.tfull[acc], acc_phase, abort_flag, p.status)) break;
+      if (!mbar_wait_warp(&ctl.tfull[acc], acc_phase, abort_flag, p.status)) break;
       tc_fence_after();
       const uint32_t t_row =
           tmem_base + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(acc * BN);

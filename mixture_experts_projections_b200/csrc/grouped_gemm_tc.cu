@@ -599,7 +599,7 @@ __global__ void __launch_bounds__(PairGeo<MODE, kQ8>::kThreads, 1)
       Part cur;
       if (kQ8) cur = next;
       else cur = part_of(tile, half);
-      if (!mbar_wait(&ctl.tfull[acc], acc_phase, abort_flag, p.status)) break;
+      if (!mbar_wait_warp(&ctl.tfull[acc], acc_phase, abort_flag, p.status)) break;
       tc_fence_after();
       if (kQ8 && item(j + 1, tile, half)) next = part_of(tile, half);
       const uint32_t t_row =
@@ -899,7 +899,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         swap_token<MODE, kQ8>(p, prow0 + lane, lane < nv, orow[0], rw[0], sa[0]);
         swap_token<MODE, kQ8>(p, prow0 + 32 + lane, 32 + lane < nv, orow[1], rw[1], sa[1]);
       }
-      if (!mbar_wait(&ctl.tfull[acc], acc_phase, abort_flag, p.status)) break;
+      if (!mbar_wait_warp(&ctl.tfull[acc], acc_phase, abort_flag, p.status)) break;
       tc_fence_after();
       const uint32_t t_row =
           tmem_base + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(acc * kAccCols);

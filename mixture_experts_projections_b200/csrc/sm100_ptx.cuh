@@ -85,6 +85,29 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity,
   }
 }
 
+// The same for a whole warp that goes on to warp-wide instructions: one answer for
+// all lanes. With an answer for each lane, a wait that runs out or another role's
+// abort while the phase completes would let some lanes leave and the others go on
+// to an instruction that needs them all.
+__device__ __forceinline__ bool mbar_wait_warp(uint64_t* bar, uint32_t parity,
+                                               volatile int* cta_abort, int* status) {
+  const uint32_t a = smem_u32(bar);
+  if (__all_sync(0xffffffffu, mbar_try_wait(a, parity))) return true;
+  const uint64_t t0 = globaltimer_ns();
+  for (uint32_t it = 1;; ++it) {
+    if (__all_sync(0xffffffffu, mbar_try_wait(a, parity))) return true;
+    if ((it & 255u) == 0) {
+      bool gone = *cta_abort != 0;
+      if (!gone && globaltimer_ns() - t0 > kWaitLimitNs) {
+        *cta_abort = 1;
+        if (status) atomicExch(status, kStatusTimeout);
+        gone = true;
+      }
+      if (__any_sync(0xffffffffu, gone)) return false;
+    }
+  }
+}
+
 // ------------------------------------------------------------------ TMA
 
 __device__ __forceinline__ void tma_prefetch_desc(const CUtensorMap* m) {

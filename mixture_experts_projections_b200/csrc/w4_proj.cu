@@ -304,9 +304,7 @@ __global__ void __maxnreg__(kTight ? 64 : 96)
       const uint4* xsrc = reinterpret_cast<const uint4*>(p.x);
       uint32_t issued = 0, last_par = 0;
       for (int kb = b0; kb < b1; kb += kW4Stage) {
-        if (!__all_sync(0xffffffffu,
-                        mbar_wait(&ctl.empty[stage], phase ^ 1u, abort_flag, p.status)))
-          break;
+        if (!mbar_wait_warp(&ctl.empty[stage], phase ^ 1u, abort_flag, p.status)) break;
         uint8_t* st = smem + stage * stage_bytes;
         if (lane == 0) {
           mbar_arrive_expect_tx(&ctl.full[stage], warps * kW4Stage * (1024 + kScaleBytes));
@@ -334,7 +332,7 @@ __global__ void __maxnreg__(kTight ? 64 : 96)
     } else {
       // ------------------------------------------------ consumers
       for (int kb = b0; kb < b1; kb += kW4Stage) {
-        if (!mbar_wait(&ctl.full[stage], phase, abort_flag, p.status)) break;
+        if (!mbar_wait_warp(&ctl.full[stage], phase, abort_flag, p.status)) break;
         const uint8_t* st = smem + stage * stage_bytes;
         const uint8_t* ws = st + warp * (kW4Stage * 1024);
         const uint8_t* ss = st + warps * (kW4Stage * 1024) + warp * (kW4Stage * kScaleBytes);
