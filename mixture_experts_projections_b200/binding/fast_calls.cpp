@@ -17,6 +17,7 @@
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
+#include <torch/version.h>
 
 #include <initializer_list>
 
@@ -285,4 +286,9 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "_fast_calls", nullptr, -1, methods
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__fast_calls() { return PyModule_Create(&module); }
+PyMODINIT_FUNC PyInit__fast_calls() {
+  PyObject* m = PyModule_Create(&module);
+  // what the loader compares with the torch that runs
+  if (m && PyModule_AddStringConstant(m, "torch_version", TORCH_VERSION) < 0) Py_CLEAR(m);
+  return m;
+}

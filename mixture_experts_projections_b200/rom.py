@@ -12,6 +12,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import warnings
 
 import torch
 
@@ -74,8 +75,8 @@ SIGNATURES = {
 }
 
 _lib = None
-# binding/fast_calls.cpp, once the library is loaded (None where it is not built:
-# the calls below then check their tensors in Python, at 0.4 us each).
+# binding/fast_calls.cpp, once the library is loaded (None where it is not built or
+# does not load: the calls below then check their tensors in Python, at 0.4 us each).
 _fast = None
 _FAST_CALLS = ("rom_add_rmsnorm", "rom_add_rmsnorm_bwd", "rom_quant_rows", "rom_expert_proj_q8",
                "rom_expert_proj_w4")
@@ -99,13 +100,20 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
             fn.argtypes = args
         _lib = lib
         if path == LIB_PATH and os.path.exists(os.path.join(_HERE, "_fast_calls.so")):
-            _load_fast_calls(lib)
+            try:
+                _load_fast_calls(lib)
+            except (ImportError, OSError) as e:
+                warnings.warn(f"{e}: tensors are checked in Python, a few microseconds per call "
+                              "more", RuntimeWarning, stacklevel=2)
     return _lib
 
 
 def _load_fast_calls(lib):
     global _fast
     from . import _fast_calls
+    if _fast_calls.torch_version != torch.__version__.split("+")[0]:
+        raise ImportError(f"_fast_calls.so was built against torch {_fast_calls.torch_version}, "
+                          f"this is {torch.__version__}")
     _fast_calls.bind(*(ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in _FAST_CALLS))
     _fast = _fast_calls
 
