@@ -80,15 +80,25 @@ struct Args {
 int dtype_code(at::ScalarType t) { return t == kBf16 ? ROM_BF16 : t == kF32 ? ROM_F32 : -1; }
 bool fits(int64_t v) { return v <= INT32_MAX; }
 
+// Lets other Python threads run: a launch blocks while the stream's queue is full,
+// and what is in the queue may be a host function that needs the lock.
+struct WithoutLock {
+  PyThreadState* state = PyEval_SaveThread();
+  ~WithoutLock() { PyEval_RestoreThread(state); }
+};
+
 template <typename F>
 PyObject* run(const Args& a, F&& f) {
   if (!a.ok) Py_RETURN_NONE;
   int status;
-  if (c10::cuda::current_device() == a.dev) {
-    status = f(c10::cuda::getCurrentCUDAStream(a.dev).stream());
-  } else {
-    c10::cuda::CUDAGuard guard(static_cast<c10::DeviceIndex>(a.dev));
-    status = f(c10::cuda::getCurrentCUDAStream(a.dev).stream());
+  {
+    WithoutLock unlocked;
+    if (c10::cuda::current_device() == a.dev) {
+      status = f(c10::cuda::getCurrentCUDAStream(a.dev).stream());
+    } else {
+      c10::cuda::CUDAGuard guard(static_cast<c10::DeviceIndex>(a.dev));
+      status = f(c10::cuda::getCurrentCUDAStream(a.dev).stream());
+    }
   }
   return PyLong_FromLong(status);
 }

@@ -1,4 +1,4 @@
-"""Calls from several host threads."""
+"""Calls from several host threads, and what they hold meanwhile."""
 import ctypes
 import threading
 
@@ -46,3 +46,22 @@ def test_norm_gradients_of_two_widths_from_two_threads():
     torch.cuda.synchronize()
     assert results == {D: {rom.ROM_OK} for D in runs}
     assert all(torch.equal(dx, ref) for _, _, dx, ref, _ in runs.values())
+
+
+@gpu
+def test_checked_calls_release_the_interpreter_lock():
+    """A launch may block (a full queue) until a host function ran that needs the
+    lock. PyGILState_Check stands in for the library's function: its status says
+    whether the caller holds the lock."""
+    lib = rom.load_library()
+    if rom._fast is None:
+        pytest.skip("the checked calls are not built")
+    held = ctypes.cast(ctypes.pythonapi.PyGILState_Check, ctypes.c_void_p).value
+    x = torch.zeros(4, 64, device="cuda")
+    q, s = torch.zeros(4, 64, dtype=torch.float8_e4m3fn, device="cuda"), torch.zeros(4, device="cuda")
+    try:
+        rom._fast.bind(*[held] * 5)
+        assert rom._fast.quant_rows(x, q, s) == 0
+    finally:
+        rom._load_fast_calls(lib)
+    assert rom._fast.quant_rows(x, q, s) == 0
