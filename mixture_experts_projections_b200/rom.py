@@ -724,8 +724,12 @@ def _inproj_forward_w4(x, w_r, w, k, renorm, bias, bufs, out, slots, stream):
     with _scope(x, stream):
         if bufs is None:
             bufs = RoutingBuffers(T, Dm, w.E, k, x.dtype, x.device)
+        else:
+            _given(bufs, dev, topk_idx=(_I32, (T, k)), topk_w=(_F32, (T, k)))
         if out is None:
             out = torch.empty((T, w.N), dtype=x.dtype, device=x.device)
+        else:
+            _t(out, "out", _BF16, (T, w.N), dev)
         if k > 1 and slots is None:
             slots = torch.empty((T * k, w.N), dtype=torch.float32, device=x.device)
         rom_route(x, w_r, bias, k, renorm, bufs.topk_idx, bufs.topk_w, None, None, stream)
@@ -743,7 +747,20 @@ def _scope(t, stream):
     """Runs the library on the device of ``t`` and on ``stream`` (None: that
     device's current one). Buffers that the functions below make belong to that
     stream, so that their memory is never still in use on another one."""
+    if stream is not None and stream.device != t.device:
+        raise RomError(f"the stream is one of {stream.device}, the call's first tensor on "
+                       f"{t.device}")
     return torch.cuda.device(t.device) if stream is None else torch.cuda.stream(stream)
+
+
+def _given(bufs, dev, **tensors):
+    """Refuses buffers of another call's sizes: those that rom_route and rom_combine
+    write, which take them as they come (name=(type, shape))."""
+    for name, (dtype, shape) in tensors.items():
+        t = getattr(bufs, name)
+        if t is None:
+            raise RomError(f"the buffers hold no {name}")
+        _t(t, name, dtype, shape, dev)
 
 
 def quant_rows(x, stream=None):
@@ -934,6 +951,10 @@ def block_forward_q8(x, w_r, bias, w_conv, w_gate, w_out, k, renorm=False, x8=No
     with _scope(x, stream):
         if bufs is None:
             bufs = Q8BlockBuffers(T, Dm, De, E, k, x.device)
+        else:
+            _given(bufs.routing, dev, topk_idx=(_I32, (T, k)), topk_w=(_F32, (T, k)),
+                   counts=(_I32, (E,)), ws=(_I32, (max(1, rom_workspace_size(T, E) // 4),)))
+            _given(bufs, dev, h_sorted=(_BF16, (T * k, De)), out=(_BF16, (T, Dm)))
         if x8 is None:
             x8, x_scale = bufs.x8, bufs.x_scale
             rom_quant_rows(x, x8, x_scale, stream)
@@ -987,6 +1008,9 @@ def block_forward_w4(x, w_r, bias, w_conv, w_gate, w_out, k, renorm=False, bufs=
     with _scope(x, stream):
         if bufs is None:
             bufs = W4BlockBuffers(T, Dm, De, k, x.device)
+        else:
+            _given(bufs, dev, topk_idx=(_I32, (T, k)), topk_w=(_F32, (T, k)),
+                   h=(_BF16, (T, De)), out=(_BF16, (T, Dm)))
         rom_route(x, w_r, bias, k, renorm, bufs.topk_idx, bufs.topk_w, None, None, stream)
         _w4_tokens(ROM_PROJ_CONV_GATE_SLOTS, x, w_conv, w_gate, k, bufs.topk_idx, bufs.topk_w,
                    bufs.uz, stream)
