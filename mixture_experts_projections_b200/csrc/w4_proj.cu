@@ -52,9 +52,20 @@ constexpr int kW4MaxSlots = kW4MaxTokens * kMaxTopK;
 constexpr int kW4MaxStages = 6;
 constexpr int kW4MostSmem = 110 * 1024;   // of each of two CTAs on an SM
 constexpr int kW4ThirdSmem = 73 * 1024;   // of each of three
-// CTAs that an SM holds: their registers set it (of one token block, 7 consumer
-// warps with 96 each or 9 with 64).
+// CTAs that an SM holds: their registers set it. Of one token block, three with up to
+// 7 consumer warps at 80 a thread, or with up to 9 at 64 (kTight); of more, two of 9
+// at 96. The kernels are bounded to these, so that it is so with any compiler.
 __host__ __device__ constexpr int w4_resident(int nb) { return nb == 1 ? 3 : 2; }
+__host__ __device__ constexpr int w4_registers(int nb, bool tight) {
+  return tight ? 64 : nb == 1 ? 80 : 96;
+}
+// (with the producer warp)
+constexpr bool w4_fits(int nb, int warps, bool tight) {
+  return w4_resident(nb) * (warps + 1) * 32 * w4_registers(nb, tight) <= 65536;
+}
+static_assert(w4_fits(1, 7, false) && w4_fits(1, kW4MaxWarps, true) && w4_fits(2, kW4MaxWarps, false) &&
+                  w4_fits(3, kW4MaxWarps, false),
+              "an SM's registers hold the CTAs that the shape of the work counts on");
 
 struct W4Params {
   const __nv_bfloat16* x;
@@ -190,7 +201,7 @@ struct W4Maps {
 // us; 14.7 with three of 7). Elsewhere the bound costs more than it gives (one
 // token, 8 experts of 4096 x 2048, top-2: 7.2 us, 6.7 without).
 template <int NB, int GS, bool kTight>
-__global__ void __maxnreg__(kTight ? 64 : 96)
+__global__ void __maxnreg__(w4_registers(NB, kTight))
     w4_proj_kernel(const __grid_constant__ W4Maps maps, const W4Params p) {
   extern __shared__ __align__(128) uint8_t smem[];
   constexpr int kTok = NB * 8;
