@@ -478,9 +478,14 @@ __device__ __forceinline__ void mbar_arrive_remote(uint32_t cluster_addr) {
                : "memory");
 }
 
-// The same to hand back a TMEM accumulator, whose reads have completed in every
-// lane (tcgen05.wait::ld, fence before the thread synchronisation): no memory of
-// the warp's is released, so the arrival does not wait for its stores.
+// The same to hand back a TMEM accumulator, whose reads have completed in every lane
+// (tcgen05.wait::ld). PTX orders tensor-memory accesses of two threads by
+// tcgen05.fence::before_thread_sync in the one, tcgen05.fence::after_thread_sync in
+// the other, and anything in between that orders their execution, for which a
+// relaxed arrival is enough. No ordinary memory of the warp's is released with it
+// (nobody reads the rows that it stored), so the arrival does not wait for those
+// stores, as a release would: Out of 16384 tokens in bf16 192.5 us, 194.5 with one;
+// top-2 Conv+Gate 809, 813.
 __device__ __forceinline__ void mbar_arrive_remote_relaxed(uint32_t cluster_addr) {
   asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr)
                : "memory");
