@@ -953,7 +953,8 @@ def block_forward_q8(x, w_r, bias, w_conv, w_gate, w_out, k, renorm=False, x8=No
             bufs = Q8BlockBuffers(T, Dm, De, E, k, x.device)
         else:
             _given(bufs.routing, dev, topk_idx=(_I32, (T, k)), topk_w=(_F32, (T, k)),
-                   counts=(_I32, (E,)), ws=(_I32, (max(1, rom_workspace_size(T, E) // 4),)))
+                   counts=(_I32, (E,)))
+            _ws(bufs.routing.ws, dev)  # (its size: rom_route)
             _given(bufs, dev, h_sorted=(_BF16, (T * k, De)), out=(_BF16, (T, Dm)))
         if x8 is None:
             x8, x_scale = bufs.x8, bufs.x_scale

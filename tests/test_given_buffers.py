@@ -72,3 +72,13 @@ def test_inproj_outputs_of_other_sizes_are_refused(block, k):
     got, _ = rom.inproj_forward(x, w_r, None, k, w_q4=w4, out=out, bufs=rom.RoutingBuffers(T, Dm, E, k, BF16, "cuda"))
     ref, _ = rom.inproj_forward(x, w_r, None, k, w_q4=w4)
     assert got is out and torch.equal(out, ref)
+
+
+@gpu
+def test_a_larger_workspace_is_taken(block):
+    """(A caller may share one over calls of several sizes.)"""
+    T, Dm, De, E, x, w_r, w = block
+    q8 = [rom.Q8Weights.quantize(t) for t in w]
+    b = rom.Q8BlockBuffers(T, Dm, De, E, 1, "cuda")
+    b.routing.ws = torch.empty(4096, dtype=torch.int32, device="cuda")
+    assert torch.equal(rom.block_forward_q8(x, w_r, None, *q8, 1, bufs=b).out, rom.block_forward_q8(x, w_r, None, *q8, 1).out)
