@@ -63,11 +63,17 @@ constexpr int kThreads = 192;
 // swap-AB kernel (weights on the MMA's M side).
 constexpr int64_t kSwapMaxRows = 1024;
 // In 8 bits, calls with at most this many routed rows per expert on average, as
-// measured (us, swap-AB against the pair kernel, K 2048, N 2048 unless stated):
-// 8 rows per expert of 8, K 4096: 12.7 / 18.4; 32 of 64, N 1024: 36 / 66; 64 of 8:
-// 14.9 / 15.1; 91 of 33, K and N 1024: 22.0 / 19.5; 128 of 8: 19.8 / 15.7. Conv+Gate
-// at N 4096: 8 of 8: 25.2 / 31.3; 32 of 8: 27.7 / 32.4; 64 of 8: 34.3 / 33.3; 128 of
-// 8: 43.6 / 34.2.
+// measured on even routings (us, swap-AB against the pair kernel, K 2048, N 2048
+// unless stated): 8 rows per expert of 8, K 4096: 12.7 / 18.4; 32 of 64, N 1024: 36 /
+// 66; 64 of 8: 14.9 / 15.1; 91 of 33, K and N 1024: 22.0 / 19.5; 128 of 8: 19.8 / 15.7.
+// Conv+Gate at N 4096: 8 of 8: 25.2 / 31.3; 32 of 8: 27.7 / 32.4; 64 of 8: 34.3 / 33.3;
+// 128 of 8: 43.6 / 34.2. The rows of each expert are on the device, so the rule goes by
+// the mean; where the rows sit on a few experts the pair kernel would be the faster
+// one, up to twice (64 experts, N 1024, weights from HBM; Out, then Conv+Gate). 64 rows
+// per expert, even: 33.9 / 38.0, 39.9 / 59.1; on half of them: 26.3 / 20.2, 36.4 / 30.3;
+// all on one: 25.7 / 13.0, 36.1 / 18.3. 32 per expert, even: 31.0 / 36.7, 37.9 / 58.2; on
+// half: 16.2 / 18.6, 22.4 / 28.4; on one: 15.7 / 11.4, 21.9 / 12.6. 96 per expert, even:
+// 46.7 / 39.1, 64.9 / 59.9; on one: 35.1 / 17.0, 49.7 / 23.9.
 constexpr int64_t kSwapMaxRowsPerExpertQ8 = 64;
 
 struct Params {

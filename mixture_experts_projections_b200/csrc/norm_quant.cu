@@ -22,8 +22,9 @@
 // read and its writes: one CTA per row, 8 columns (16 bytes of bf16) per
 // thread and step, V steps; short rows take a warp or a part of one. The choice
 // goes by the row's length alone, so a row's result does not depend on the batch.
-// 16384 x 2048 bf16 with a float32 residual and 8-bit rows: 66 us, the 437 MB at
-// the measured copy rate; the gradient of 32768 x 2560 bf16: 135 us (128).
+// 16384 x 2048 bf16 with a float32 residual and 8-bit rows: 66 us in a graph (68 as
+// called from Python), the 437 MB at the measured copy rate; the gradient of 32768 x
+// 2560 bf16 with a bf16 residual: 134 us (128).
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 
@@ -308,8 +309,9 @@ __global__ void __launch_bounds__(512)
 // registers for it (with its loads after the sum's barrier, and none ahead, the
 // kernel took 179 us for 32768 x 2560 bf16 where the bytes take 128). Longer rows
 // of a bf16 stream wait in shared memory, each thread's own pieces (5000 x 16384:
-// 136 us, 237 without; 125 by the bytes). Those of a float32 stream do not: all three
-// inputs there leave the weights no L1 (319 us, 281 without; 200 by the bytes).
+// 138 us, 237 without; 125 by the bytes). Those of a float32 stream do not: all three
+// inputs there leave the weights no L1 (bf16 rows of 16384 columns: 319 us, 282
+// without; 200 by the bytes).
 // Short rows leave room for several in a CTA, each with threads of its own
 // (blockDim.y of them; 8, 16 or 32 lanes of a warp for up to 64, 128 or 512
 // columns, kLanes): the CTA's sums of dw are theirs, added in order. With one row
@@ -486,7 +488,7 @@ __global__ void __launch_bounds__(
 // kCols rows at a time, and the sums of 32 warps are added in a fixed order. 8
 // columns (a 32-byte sector of a row) while that leaves at most two CTAs per SM,
 // else 32: the gradient of 11564 x 112 takes 6.0 us with 8, 6.5 with 32; that of
-// 4096 x 8192 bf16 96.9 with 8, 91.4 with 32.
+// 4096 x 8192 bf16 with a float32 residual 96.9 with 8, 90.4 with 32 (82 by the bytes).
 template <int kCols>
 __global__ void __launch_bounds__(1024)
     dw_reduce_kernel(const float* __restrict__ part, int P, int D, float* __restrict__ dw) {

@@ -11,10 +11,11 @@
 // read, once for up to 24 of their tokens. The matrix instruction is the
 // warp-level m16n8k16: its A operand (16 weight rows) comes from registers, so a
 // code goes from the loaded word to the tensor core without a pass through
-// shared memory. tcgen05 measured slower here: with the weights in TMEM as A
-// (M = 128) an MMA of 16 or 32 tokens takes 60 cycles to issue, 8 per 128 x 128
-// block, and every unit of 128 rows waits for its accumulators (63 us for 64
-// tokens over 4 experts of 10240 x 4096 against 36). The codes are integers
+// shared memory. One form on tcgen05 was measured, and slower: with the weights in
+// TMEM as A (M = 128) an MMA of 16 or 32 tokens takes 60 cycles to issue, 8 per 128 x
+// 128 block, and every unit of 128 rows waits for its accumulators (63 us for 64
+// tokens over 4 experts of 10240 x 4096, this kernel 34 to 36). Weights unpacked into
+// shared memory for it were not tried. The codes are integers
 // -8 .. 7, exact in bf16; products with bf16 activations are exact in float32,
 // sums are float32, and a group's sum is multiplied by its scale in float32.
 //
@@ -207,7 +208,7 @@ struct W4Maps {
 //
 // kTight: 64 registers, for three CTAs of 8 or 9 consumer warps on an SM where
 // there are as many (19 tokens, top-2 of 16 experts of 2004 x 1000, Conv+Gate: 12.9
-// us; 14.7 with three of 7). Elsewhere the bound costs more than it gives (one
+// us; 14.7 with three of 7; both called in a loop, the weights in L2). Elsewhere the bound costs more than it gives (one
 // token, 8 experts of 4096 x 2048, top-2: 7.2 us, 6.7 without).
 template <int NB, int GS, bool kTight>
 __global__ void __maxnreg__(w4_registers(NB, kTight))
@@ -614,10 +615,12 @@ cudaError_t launch_w4_proj(const void* x, int T, int K, const void* q0, const vo
   // where few warps are resident, and the cluster's hand-over of its sums, in
   // tiles (fewer where a tile takes longer for its tokens). The constants are the
   // best of a grid over 75 shapes timed in every form, 3 % above the best form on
-  // average, geometrically. Measured, us, at 4 experts of 10240 x 4096: one token
-  // 10.7 (9 warps, 2 splits; 12.6 with 4 and 1, 14.0 with 9 and 4), 64 tokens 36.3
-  // (9 and 1; 44 with 5, 47 with 8); 4 experts of 154 x 3960, 30 tokens, top-3: 9.3
-  // (4 and 8; 14.2 with 4 and 2).
+  // average, geometrically; each shape in a loop on one set of weights, most of which
+  // fit L2. Measured so, us, at 4 experts of 10240 x 4096: one token 10.7 (9 warps, 2
+  // splits; 12.6 with 4 and 1, 14.0 with 9 and 4), 64 tokens 36.3 (9 and 1; 44 with 5,
+  // 47 with 8; later changes brought the 36.3 to 34.3); 4 experts of 154 x 3960, 30 tokens,
+  // top-3: 9.3 (4 and 8; 14.2 with 4 and 2). With every call's weights from HBM the
+  // chosen forms take 11.8, 35.8 and 12.2; the others were not timed so.
   const double used = std::ceil(E * (1.0 - std::pow(1.0 - static_cast<double>(k) / E, T)) - 0.1);
   const double blocks = std::max(1.0, static_cast<double>(T) * k / used / 8.0);
   const double hand_over = 96.0 / std::sqrt(blocks);
