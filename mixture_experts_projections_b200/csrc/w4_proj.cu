@@ -208,8 +208,9 @@ struct W4Maps {
 //
 // kTight: 64 registers, for three CTAs of 8 or 9 consumer warps on an SM where
 // there are as many (19 tokens, top-2 of 16 experts of 2004 x 1000, Conv+Gate: 12.9
-// us; 14.7 with three of 7; both called in a loop, the weights in L2). Elsewhere the bound costs more than it gives (one
-// token, 8 experts of 4096 x 2048, top-2: 7.2 us, 6.7 without).
+// us; 14.7 with three of 7; both called in a loop, the weights in L2). Elsewhere the
+// bound costs more than it gives (one token, 8 experts of 4096 x 2048, top-2: 7.2 us,
+// 6.7 without).
 template <int NB, int GS, bool kTight>
 __global__ void __maxnreg__(w4_registers(NB, kTight))
     w4_proj_kernel(const __grid_constant__ W4Maps maps, const W4Params p) {

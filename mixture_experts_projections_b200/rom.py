@@ -111,9 +111,10 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
 def _load_fast_calls(lib):
     global _fast
     from . import _fast_calls
-    if _fast_calls.torch_version != torch.__version__.split("+")[0]:
-        raise ImportError(f"_fast_calls.so was built against torch {_fast_calls.torch_version}, "
-                          f"this is {torch.__version__}")
+    built = getattr(_fast_calls, "torch_version", "unknown")
+    if not torch.__version__.startswith(built):
+        raise ImportError(f"_fast_calls.so was built against torch {built}, this is "
+                          f"{torch.__version__}")
     _fast_calls.bind(*(ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in _FAST_CALLS))
     _fast = _fast_calls
 
