@@ -188,7 +188,8 @@ int rom_expert_proj(int proj, int dtype, const void* a_sorted, int64_t R, int K,
  * rom_expert_proj. Nothing before the epilogue depends on the routing, so
  * the kernel is launched as a programmatic dependent of the kernel before it
  * on the stream (the router: decode steps need no rom_dispatch) and only its
- * epilogue waits for that kernel's results.
+ * epilogue waits for that kernel's results. So x and w may not be what that
+ * kernel writes: where rom_add_rmsnorm makes x, rom_route(x) stands in between.
  *
  *  proj      ROM_PROJ_INPROJ or ROM_PROJ_OUT (both weighted by r), optionally
  *            | ROM_W_TILED
